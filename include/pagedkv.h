@@ -13,10 +13,12 @@
  *  3. paged_gqa_decode_step: 1 and 2 in one launch.
  * and around them: fused_add_rmsnorm_qkv, the residual add, RMSNorm and QKV
  * projection that produce the step's q and new K/V; paged_kv_fp8_scales and
- * the *_fp8_scaled variants, FP8 caches with scales on the device; and
+ * the *_fp8_scaled variants, FP8 caches with scales on the device;
  * paged_gqa_prefill_attention, many query tokens per sequence over the same
  * paged cache (chunked prefill), load-balanced over the SMs when given the
- * workspace paged_gqa_prefill_workspace_size names.
+ * workspace paged_gqa_prefill_workspace_size names; paged_kv_rope_cache_write,
+ * rotary positions and the cache write in one launch; paged_kv_cache_read; and
+ * the *_int8 calls, an 8-bit cache with a scale per token and KV head.
  *
  * Sources, cited by page title and section:
  *  - "rvLLM 소개" (discuss.pytorch.kr), §PagedAttention과 FlashAttention-3:
@@ -85,7 +87,9 @@ typedef enum {
 
 typedef enum {
     PKV_KV_F16 = 0,            /* float16 cache */
-    PKV_KV_FP8_E4M3 = 1        /* uint8 OCP E4M3 cache, per-tensor or per-KV-head scales */
+    PKV_KV_FP8_E4M3 = 1,       /* uint8 OCP E4M3 cache, per-tensor or per-KV-head scales */
+    PKV_KV_INT8 = 2            /* uint8 cache, one scale per (slot, KV head); only the calls that
+                                  name it take it */
 } pkv_kv_dtype;
 
 /* partition_tokens value that lets the library plan the split-KV work: the
@@ -112,7 +116,8 @@ typedef enum {
 #define PKV_DEVERR_SLOT          0x4u  /* a slot lay outside the pool; the token was skipped */
 #define PKV_DEVERR_WAIT_TIMEOUT  0x8u  /* an on-chip barrier wait ran out of its time limit */
 #define PKV_DEVERR_SCALE         0x10u /* a device-side FP8 scale was not positive and finite;
-                                          the results that used it are undefined */
+                                          the results that used it are undefined (8-bit
+                                          cache: a scale outside [0, 2^60], taken as 0) */
 
 /*
  * paged_kv_cache_write -- reshape_and_cache.
@@ -505,6 +510,153 @@ pkv_status paged_gqa_decode_step_fp8_scaled(
     int32_t max_context_len, float softmax_scale,
     const float* k_scales, const float* v_scales, int32_t scales_per_head,
     void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache (PKV_KV_INT8): a scale per token and KV head.
+ *
+ * k_cache, v_cache [num_blocks, 16, Hkv, 128] uint8, and kv_scales
+ * [num_blocks, Hkv, 2, 16] float32 (16-byte aligned): the K scales, then the V
+ * scales, of the 16 tokens of one page and KV head. A code c with scale s
+ * stands for (c - 128) * s. The write takes, per (token, KV head) and for K
+ * and V apart, over the 128 channels x:
+ *   s = max(amax, 2^-24) / 127          (fp32 division; amax over the finite
+ *                                        channels)
+ *   c = 128 + clamp(round(x / s), -127, 127)   (fp32 division, nearest even;
+ *                                        infinities clamp, NaN stores 128)
+ * so every token keeps 8 bits of its own range, where one scale for the whole
+ * cache (FP8) leaves an element 4 significant bits: half a step is amax / 254.
+ * A page and head is 4 KiB of codes and 128 bytes of scales.
+ *
+ * Scales read by the attention must lie in [0, 2^60] for tokens inside a
+ * context; others are flagged (PKV_DEVERR_SCALE) and count as 0, a row of
+ * zeros. Rows past a context may hold anything, NaN scales included.
+ */
+
+/*
+ * paged_kv_cache_write_int8 -- paged_kv_cache_write into an 8-bit cache: the
+ * rows named by slot_mapping get the codes above, kv_scales their scales.
+ * Negative slots are skipped, slots outside the pool skipped and flagged. Two
+ * tokens with the same slot: unspecified, and codes and scale may come from
+ * different ones.
+ */
+pkv_status paged_kv_cache_write_int8(const void* k_new, const void* v_new,
+                                     void* k_cache, void* v_cache, float* kv_scales,
+                                     const int64_t* slot_mapping,
+                                     int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t num_blocks, int32_t block_size, void* stream);
+
+/*
+ * paged_kv_cache_read -- the inverse of the writes, for every cache type:
+ * k_out[i], v_out[i] ([T, Hkv, 128] f16) are the values of slot
+ * slot_mapping[i]: f16 copied; FP8 decoded * k_scale (v_scale); 8-bit
+ * (code - 128) * scale; the products in fp32, rounded once to f16. A slot may
+ * be read more than once. Negative slots leave their rows of the outputs as
+ * they were; so do slots outside the pool, which are flagged. kv_scales is
+ * read for PKV_KV_INT8 only. head_dim == 128; block_size 16 for PKV_KV_INT8.
+ */
+pkv_status paged_kv_cache_read(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const float* kv_scales, const int64_t* slot_mapping,
+                               int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t num_blocks, int32_t block_size,
+                               int32_t kv_dtype, float k_scale, float v_scale, void* stream);
+
+/* flags of paged_kv_rope_cache_write */
+#define PKV_ROPE_INTERLEAVED 0x1u   /* channels 2j, 2j+1 form pair j (else j, j + rotary_dim/2) */
+#define PKV_ROPE_CYCLIC_AXES 0x2u   /* frequencies go round the axes (else in runs) */
+
+/*
+ * paged_kv_rope_cache_write -- rotary positions and the cache write in one
+ * launch: q_out is q rotated (f16), and K rotated and V as given are stored at
+ * slot_mapping as the cache writes store them, in an f16, FP8 or 8-bit cache.
+ *
+ * Pair j < rotary_dim / 2 of a head, (x, y), becomes
+ *   (x cos a - y sin a, y cos a + x sin a),  a = positions[axis(j)][t] * inv_freq[j].
+ * Channels from rotary_dim on are left as they are. With num_axes == 1 that is
+ * the usual rotary embedding; with several axes (time, height and width of an
+ * image or video token; at most 4) axis_sections (a HOST array of num_axes
+ * counts that sum to rotary_dim / 2) shares the frequencies out:
+ *   in runs:  the first axis_sections[0] belong to axis 0, the next
+ *             axis_sections[1] to axis 1, ...;
+ *   cyclic:   j belongs to axis a = j mod num_axes when a > 0 and
+ *             j < num_axes * axis_sections[a], else to axis 0.
+ * Angles are formed in fp64 and reduced before the sine and cosine, so
+ * positions as far as 2^31 keep fp32 accuracy. The rotation is fp32 and is
+ * rounded once, to the f16 of q_out or to the cache's type (an 8-bit or FP8
+ * cache quantises the unrounded fp32 values).
+ *
+ * q, q_out [T, Hq, 128] f16, q_out may be q (num_q_heads may be 0: neither is
+ * then read); k_new, v_new [T, Hkv, 128] f16; positions [num_axes, T] int64;
+ * inv_freq [rotary_dim / 2] float32, on the device. rotary_dim is a multiple
+ * of 16. Negative slots skip the cache write only: q_out is written for every
+ * token. kv_scales is used for PKV_KV_INT8, k_scale and v_scale for
+ * PKV_KV_FP8_E4M3. Slot errors and duplicates are as in the cache writes.
+ */
+pkv_status paged_kv_rope_cache_write(void* q_out, const void* q, const void* k_new, const void* v_new,
+                                     void* k_cache, void* v_cache, float* kv_scales,
+                                     const int64_t* slot_mapping, const int64_t* positions,
+                                     const float* inv_freq,
+                                     int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t rotary_dim, int32_t num_axes,
+                                     const int32_t* axis_sections,
+                                     int32_t num_blocks, int32_t block_size,
+                                     int32_t kv_dtype, float k_scale, float v_scale,
+                                     uint32_t flags, void* stream);
+
+/* paged_kv_rope_cache_write into an FP8 cache with device-side scales, one or
+ * one per KV head, as paged_kv_cache_write_fp8_scaled takes them. */
+pkv_status paged_kv_rope_cache_write_fp8_scaled(
+    void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+    const int64_t* slot_mapping, const int64_t* positions, const float* inv_freq,
+    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t rotary_dim, int32_t num_axes, const int32_t* axis_sections,
+    int32_t num_blocks, int32_t block_size,
+    const float* k_scales, const float* v_scales, int32_t scales_per_head,
+    uint32_t flags, void* stream);
+
+/*
+ * Bytes of workspace paged_gqa_decode_attention_int8 needs on the CURRENT
+ * device, whatever the sizes (0 on error).
+ */
+size_t paged_gqa_decode_workspace_size_int8(void);
+
+/*
+ * paged_gqa_decode_attention_int8 -- paged_gqa_decode_attention over an 8-bit
+ * cache, always load-balanced (the plan of PKV_PARTITION_AUTO). `workspace`
+ * is required, 256-byte aligned, zero-filled before its first use, and left
+ * ready for the next call, as there; calls that share one must not run
+ * concurrently (two captured graphs that share one must not be replayed at the
+ * same time either). The workspace of paged_gqa_prefill_workspace_size(...,
+ * PKV_KV_INT8) serves this call too. Batches above 8192 sequences, and batches
+ * of 2^31 or more (sequence, KV head, page) units, return
+ * PKV_ERR_UNSUPPORTED.
+ */
+pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                           const float* kv_scales,
+                                           const int32_t* block_tables, const int32_t* context_lens,
+                                           int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t block_size,
+                                           int32_t max_blocks_per_seq, int32_t num_blocks,
+                                           int32_t max_context_len, float softmax_scale,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * paged_gqa_prefill_attention_int8 -- paged_gqa_prefill_attention (several new
+ * query tokens per sequence, the last ones of its context, causal) over an
+ * 8-bit cache: from a few drafted tokens per sequence to long prefill chunks.
+ * `workspace` (paged_gqa_prefill_workspace_size(..., PKV_KV_INT8) bytes) is
+ * required, with the rules of paged_gqa_decode_attention_int8; so are its
+ * limits on the batch, counted with the query groups a long chunk is cut into.
+ * Sequences with inconsistent lengths are flagged and their rows left alone.
+ */
+pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                            const float* kv_scales,
+                                            const int32_t* block_tables, const int32_t* context_lens,
+                                            const int32_t* query_start,
+                                            int32_t batch, int32_t total_queries, int32_t max_query_len,
+                                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                            int32_t block_size, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                            int32_t max_context_len, float softmax_scale,
+                                            void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,6 +16,8 @@ Tensors are torch CUDA tensors used as plain device memory:
   slot_mapping      [T]                     int64
   query_start       [B + 1]                 int32 (prefill)
   x, residual       [T, H]                  float16 (QKV projection; w_qkv [N, H], gamma [H])
+  kv_scales         [NB, Hkv, 2, 16]        float32 (8-bit cache: scale per token and KV head, K then V)
+  positions         [axes, T] or [T]        int64 (rotary cache write; inv_freq [rotary_dim / 2] float32)
 """
 from __future__ import annotations
 
@@ -56,6 +58,22 @@ _SIGNATURES = {
     "paged_gqa_prefill_workspace_size": ([_i32, _i32, _i32, _i32], _sz),
     "paged_gqa_prefill_attention": ([_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                      _i32, _i32, _i32, _f32, _i32, _f32, _f32, _P, _sz, _P], ctypes.c_int),
+    "paged_kv_cache_write_int8": ([_P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P], ctypes.c_int),
+    "paged_kv_cache_read": ([_P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _P],
+                            ctypes.c_int),
+    "paged_kv_rope_cache_write": (
+        [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _P, _i32, _i32, _i32, _f32,
+         _f32, ctypes.c_uint32, _P], ctypes.c_int),
+    "paged_kv_rope_cache_write_fp8_scaled": (
+        [_P, _P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _P, _i32, _i32, _P, _P, _i32,
+         ctypes.c_uint32, _P], ctypes.c_int),
+    "paged_gqa_decode_workspace_size_int8": ([], _sz),
+    "paged_gqa_decode_attention_int8": (
+        [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P],
+        ctypes.c_int),
+    "paged_gqa_prefill_attention_int8": (
+        [_P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz,
+         _P], ctypes.c_int),
 }
 # The symbols include/pagedkv.h declares (checked by the CPU tests).
 EXPORTED = tuple(_SIGNATURES)
@@ -87,12 +105,14 @@ def __getattr__(name):
 
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA = range(5)
-PKV_KV_F16, PKV_KV_FP8_E4M3 = 0, 1
+PKV_KV_F16, PKV_KV_FP8_E4M3, PKV_KV_INT8 = 0, 1, 2
 PKV_PARTITION_AUTO = -1         # partition_tokens: the library's load-balanced plan
 PKV_STEP_OVERLAP_PREVIOUS = 0x1  # paged_gqa_decode_step flag (see include/pagedkv.h)
 PKV_STEP_SELFTEST_WAIT_TIMEOUT = 0x100  # self-test: one worker loads nothing, its wait runs out
 DEVERR_CONTEXT_LEN, DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_WAIT_TIMEOUT, DEVERR_SCALE = 0x1, 0x2, 0x4, 0x8, 0x10
+PKV_ROPE_INTERLEAVED, PKV_ROPE_CYCLIC_AXES = 0x1, 0x2   # paged_kv_rope_cache_write flags
 _KV_DTYPES = {"f16": PKV_KV_F16, "fp8": PKV_KV_FP8_E4M3}
+_CACHE_DTYPES = {**_KV_DTYPES, "int8": PKV_KV_INT8}     # of the calls that take every cache type
 
 
 class PagedKVError(RuntimeError):
@@ -380,9 +400,10 @@ def fused_add_rmsnorm_qkv_plan(T, H, Hq, Hkv, D) -> dict:
 
 
 def paged_gqa_prefill_workspace_size(num_q_heads, num_kv_heads, head_dim, kv_dtype="f16") -> int:
-    """Bytes of workspace for the load-balanced prefill schedule on the current device (0: none)."""
-    return int(load_library().paged_gqa_prefill_workspace_size(num_q_heads, num_kv_heads, head_dim,
-                                                                kv_dtype_code(kv_dtype)))
+    """Bytes of workspace for the load-balanced prefill schedule on the current device (0: none);
+    kv_dtype "int8": of paged_gqa_prefill_attention_int8."""
+    code = PKV_KV_INT8 if kv_dtype == "int8" else kv_dtype_code(kv_dtype)
+    return int(load_library().paged_gqa_prefill_workspace_size(num_q_heads, num_kv_heads, head_dim, code))
 
 
 def paged_gqa_prefill_attention(out, q, k_cache, v_cache, block_tables, context_lens, query_start, *,
@@ -412,3 +433,179 @@ def paged_gqa_prefill_attention(out, q, k_cache, v_cache, block_tables, context_
         B, total, int(max_query_len), Hq, Hkv, D, bs, block_tables.shape[1], NB, int(max_context_len),
         float(softmax_scale), kv_dtype_code(kv_dtype), float(k_scale), float(v_scale), _ptr(workspace), ws_bytes,
         _stream(stream)), "paged_gqa_prefill_attention")
+
+
+# ----------------------------------------------------------------------------
+# The 8-bit cache (a scale per token and KV head), rotary positions with the
+# cache write, and reading a cache back.
+
+def _here(*tensors):
+    """Checks that the tensors are on the current device: launches go to its current stream."""
+    import torch
+    for t in tensors:
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _shapes(**named):
+    """Checks (tensor, shape) pairs given by name."""
+    for name, (t, shape) in named.items():
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cache(k_cache, v_cache, kv_dtype, kv_scales=None):
+    """Checks a cache of any type; its (num_blocks, block_size, Hkv, D) and type code."""
+    if kv_dtype not in _CACHE_DTYPES:
+        raise ValueError(f"kv_dtype must be one of {sorted(_CACHE_DTYPES)}")
+    dtype = "float16" if kv_dtype == "f16" else "uint8"
+    _dense("k_cache", k_cache, dtype)
+    _dense("v_cache", v_cache, dtype)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    NB, bs, Hkv, D = k_cache.shape
+    _shapes(v_cache=(v_cache, k_cache.shape))
+    if kv_dtype == "int8":
+        if kv_scales is None:
+            raise ValueError("an int8 cache needs kv_scales")
+        _dense("kv_scales", kv_scales, "float32")
+        _shapes(kv_scales=(kv_scales, (NB, Hkv, 2, bs)))
+    elif kv_scales is not None:
+        raise ValueError("kv_scales belongs to an int8 cache")
+    _here(k_cache, v_cache, kv_scales)
+    return NB, bs, Hkv, D, _CACHE_DTYPES[kv_dtype]
+
+
+def _rows(name, t, T, H, D):
+    _dense(name, t, "float16")
+    _shapes(**{name: (t, (T, H, D))})
+    _here(t)
+
+
+def paged_kv_cache_write_int8(k_new, v_new, k_cache, v_cache, kv_scales, slot_mapping, *, stream=None) -> None:
+    """paged_kv_cache_write into an 8-bit cache: codes 128 + round(x / s) (uint8) and, in
+    kv_scales [NB, Hkv, 2, 16] float32, s = max(max|x|, 2**-24) / 127 of every token and KV head."""
+    NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales)
+    _dense("slot_mapping", slot_mapping, "int64")
+    T = slot_mapping.numel()
+    _rows("k_new", k_new, T, Hkv, D)
+    _rows("v_new", v_new, T, Hkv, D)
+    _here(slot_mapping)
+    _check(load_library().paged_kv_cache_write_int8(
+        _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(slot_mapping), T, Hkv, D, NB,
+        bs, _stream(stream)), "paged_kv_cache_write_int8")
+
+
+def paged_kv_cache_read(k_out, v_out, k_cache, v_cache, slot_mapping, *, kv_dtype="f16", kv_scales=None,
+                        k_scale=1.0, v_scale=1.0, stream=None) -> None:
+    """k_out[i], v_out[i] ([T, Hkv, D] float16) = the cached values of slot slot_mapping[i], for an
+    "f16", "fp8" or "int8" cache. Rows of negative slots are left as they were."""
+    NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales)
+    _dense("slot_mapping", slot_mapping, "int64")
+    T = slot_mapping.numel()
+    _rows("k_out", k_out, T, Hkv, D)
+    _rows("v_out", v_out, T, Hkv, D)
+    _here(slot_mapping)
+    _check(load_library().paged_kv_cache_read(
+        _ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(slot_mapping), T, Hkv, D, NB,
+        bs, code, float(k_scale), float(v_scale), _stream(stream)), "paged_kv_cache_read")
+
+
+def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq, *,
+                              sections=None, interleaved=False, cyclic_axes=False, kv_dtype="f16", kv_scales=None,
+                              k_scale=1.0, v_scale=1.0, stream=None) -> None:
+    """Rotary positions and the cache write in one launch: q_out = q rotated (q_out may be q), and
+    k_new rotated and v_new go to their slots of an "f16", "fp8" or "int8" cache.
+
+    positions [T] or [axes, T] int64; inv_freq [rotary_dim / 2] float32 (rotary_dim a multiple of 16,
+    channels past it are left as they are). `sections`: frequencies per axis (default: one axis), in
+    runs, or round the axes (cyclic_axes). `interleaved`: channels (2j, 2j + 1) form a pair, else
+    (j, j + rotary_dim / 2). For an "fp8" cache k_scale and v_scale are numbers, or float32 CUDA
+    tensors of 1 or Hkv elements.
+    """
+    NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales)
+    _dense("slot_mapping", slot_mapping, "int64")
+    _dense("positions", positions, "int64")
+    _dense("inv_freq", inv_freq, "float32")
+    T = slot_mapping.numel()
+    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions must be [{T}] or [axes, {T}], got {tuple(positions.shape)}")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    half = inv_freq.numel()
+    sections = [half] if sections is None else [int(n) for n in sections]
+    if len(sections) != axes:
+        raise ValueError(f"{len(sections)} sections for {axes} position axes")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, num_q_heads, head_dim]")
+    Hq = q.shape[1]
+    _rows("q", q, T, Hq, D)
+    _rows("q_out", q_out, T, Hq, D)
+    _rows("k_new", k_new, T, Hkv, D)
+    _rows("v_new", v_new, T, Hkv, D)
+    _here(slot_mapping, positions, inv_freq)
+    flags = (PKV_ROPE_INTERLEAVED if interleaved else 0) | (PKV_ROPE_CYCLIC_AXES if cyclic_axes else 0)
+    host_sections = (ctypes.c_int32 * max(axes, 1))(*sections)
+    head = (_ptr(q_out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache))
+    sizes = (_ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), T, Hq, Hkv, D, 2 * half, axes, host_sections, NB, bs)
+    if kv_dtype == "fp8" and hasattr(k_scale, "data_ptr"):
+        per_head = _scales(k_scale, v_scale, Hkv)
+        _here(k_scale, v_scale)
+        _check(load_library().paged_kv_rope_cache_write_fp8_scaled(
+            *head, *sizes, _ptr(k_scale), _ptr(v_scale), per_head, flags, _stream(stream)),
+            "paged_kv_rope_cache_write_fp8_scaled")
+        return
+    _check(load_library().paged_kv_rope_cache_write(
+        *head, _ptr(kv_scales), *sizes, code, float(k_scale), float(v_scale), flags, _stream(stream)),
+        "paged_kv_rope_cache_write")
+
+
+def paged_gqa_decode_workspace_size_int8() -> int:
+    """Bytes of workspace of paged_gqa_decode_attention_int8 on the current device, whatever the sizes."""
+    return int(load_library().paged_gqa_decode_workspace_size_int8())
+
+
+def _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace):
+    NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [rows, num_q_heads, head_dim] and block_tables [batch, max_blocks]")
+    rows, Hq, _ = q.shape
+    _rows("q", q, rows, Hq, D)
+    _rows("out", out, rows, Hq, D)
+    _dense("block_tables", block_tables, "int32")
+    _dense("context_lens", context_lens, "int32")
+    _dense("workspace", workspace, "uint8", "float32", "int32")
+    B = block_tables.shape[0]
+    _shapes(context_lens=(context_lens, (B,)))
+    _here(block_tables, context_lens, workspace)
+    return rows, Hq, Hkv, D, NB, bs, B, workspace.numel() * workspace.element_size()
+
+
+def paged_gqa_decode_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, *,
+                                    max_context_len, softmax_scale, workspace, stream=None) -> None:
+    """paged_gqa_decode_attention over an 8-bit cache (load-balanced plan; a zero-filled workspace of
+    paged_gqa_decode_workspace_size_int8() bytes, reusable)."""
+    rows, Hq, Hkv, D, NB, bs, B, ws_bytes = _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables,
+                                                            context_lens, workspace)
+    if rows != B:
+        raise ValueError(f"{rows} query rows for {B} sequences")
+    _check(load_library().paged_gqa_decode_attention_int8(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(block_tables), _ptr(context_lens),
+        B, Hq, Hkv, D, bs, block_tables.shape[1], NB, int(max_context_len), float(softmax_scale), _ptr(workspace),
+        ws_bytes, _stream(stream)), "paged_gqa_decode_attention_int8")
+
+
+def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, *,
+                                     max_query_len, max_context_len, softmax_scale, workspace, stream=None) -> None:
+    """paged_gqa_prefill_attention over an 8-bit cache: query rows q [total, Hq, D] of each sequence
+    (query_start [B+1] int32), the last n_b tokens of its context, attending causally; a zero-filled
+    workspace of paged_gqa_prefill_workspace_size(Hq, Hkv, D, "int8") bytes, reusable."""
+    rows, Hq, Hkv, D, NB, bs, B, ws_bytes = _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables,
+                                                            context_lens, workspace)
+    _dense("query_start", query_start, "int32")
+    _shapes(query_start=(query_start, (B + 1,)))
+    _here(query_start)
+    _check(load_library().paged_gqa_prefill_attention_int8(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(block_tables), _ptr(context_lens),
+        _ptr(query_start), B, rows, int(max_query_len), Hq, Hkv, D, bs, block_tables.shape[1], NB,
+        int(max_context_len), float(softmax_scale), _ptr(workspace), ws_bytes, _stream(stream)),
+        "paged_gqa_prefill_attention_int8")

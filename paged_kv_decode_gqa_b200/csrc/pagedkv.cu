@@ -20,6 +20,8 @@
 #include "qkv_proj.cuh"
 #include "prefill_attention.cuh"
 #include "prefill_tc.cuh"
+#include "int8_cache.cuh"
+#include "stream_int8.cuh"
 
 namespace {
 
@@ -773,6 +775,224 @@ bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// ------------------------------------------- 8-bit cache, rotary cache write
+constexpr int kStreamWarps1 = 12, kStreamStages1 = 3;   // one column tile (decode)
+constexpr int kStreamWarpsN = 8, kStreamStagesN = 3;    // several (short chunks)
+constexpr int kStreamMaxTiles = 4;
+
+// kv_scales [NB, Hkv, 2, 16] fp32 as a 3-D tensor (32 scales, head, block), one
+// box = the 32 scales of a page and head; blocks outside the pool read zeros.
+bool make_scale_map(CUtensorMap* map, const void* base, int num_blocks, int Hkv) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    if (!encode) return false;
+    cuuint64_t dims[3] = {32, (cuuint64_t)Hkv, (cuuint64_t)num_blocks};
+    cuuint64_t strides[2] = {128, (cuuint64_t)Hkv * 128};
+    cuuint32_t box[3] = {32u, 1u, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool cached_scale_map(CUtensorMap* out, const void* base, int num_blocks, int Hkv) {
+    constexpr int kSlots = 8;
+    thread_local MapKey keys[kSlots];
+    thread_local CUtensorMap maps[kSlots];
+    thread_local int used = 0, next = 0;
+    const MapKey key{base, num_blocks, Hkv, false};
+    for (int i = 0; i < used; ++i)
+        if (keys[i] == key) {
+            *out = maps[i];
+            return true;
+        }
+    CUtensorMap m;
+    if (!make_scale_map(&m, base, num_blocks, Hkv)) return false;
+    keys[next] = key;
+    maps[next] = m;
+    next = (next + 1) % kSlots;
+    used = std::min(used + 1, kSlots);
+    *out = m;
+    return true;
+}
+
+int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+// Workspace of the streaming kernel for `tiles` column tiles: the merge tickets
+// first, at the same place whatever the plan (they are zero between calls, so
+// calls of every plan can share a workspace), then (m, l) and O of two pieces
+// per worker warp.
+struct StreamWorkspace {
+    size_t tickets, ml, o, total;
+};
+StreamWorkspace stream_workspace(int sms, int tiles) {
+    const size_t slots = 2 * (size_t)sms * (tiles == 1 ? kStreamWarps1 : kStreamWarpsN);
+    StreamWorkspace w;
+    w.tickets = 0;
+    w.ml = align256(pkv::kMergeLevels * 2 * (size_t)sms * std::max(kStreamWarps1, kStreamWarpsN) * sizeof(unsigned int));
+    w.o = w.ml + align256(slots * tiles * 4 * sizeof(float4));
+    w.total = w.o + slots * tiles * 256 * sizeof(float4);
+    return w;
+}
+
+// Column tiles of a chunk call: enough for the longest chunk's (query, head)
+// columns, at most kStreamMaxTiles (longer chunks take several query groups).
+int stream_tiles(int max_query_len, int G) {
+    return (int)std::min<int64_t>(kStreamMaxTiles, ((int64_t)max_query_len * G + 7) / 8);
+}
+
+template <int kNT>
+pkv_status launch_stream_int8(const pkv::StreamInt8Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
+                              const CUtensorMap& ms, int sms, cudaStream_t st) {
+    constexpr int kWarps = kNT == 1 ? kStreamWarps1 : kStreamWarpsN;
+    constexpr int kStages = kNT == 1 ? kStreamStages1 : kStreamStagesN;
+    using S = pkv::StreamInt8Shape<kNT, kWarps, kStages>;
+    auto kernel = pkv::stream_int8_kernel<kNT, kWarps, kStages>;
+    static unsigned long long done = 0;
+    if (ensure_smem(kernel, (int)S::smem_bytes(kBalMaxBatch), &done) != cudaSuccess) return PKV_ERR_CUDA;
+    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::kThreads), S::smem_bytes(prm.B), st, mk, mv, ms, prm) ==
+                   cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// Decode (query_start null) and short chunks over the 8-bit cache.
+pkv_status stream_int8(pkv::StreamInt8Params prm, const void* k_cache, const void* v_cache, const float* kv_scales,
+                       void* workspace, size_t workspace_bytes, cudaStream_t st) {
+    const bool chunked = prm.query_start != nullptr;
+    const int tiles = chunked ? stream_tiles(prm.max_query_len, prm.G) : 1;
+    prm.queries_per_group = chunked ? 8 * tiles / prm.G : 1;
+    prm.min_units_per_worker = kBalMinUnits;
+    // units of the batch are numbered in 32 bits
+    const int64_t groups = chunked ? (prm.max_query_len + prm.queries_per_group - 1) / prm.queries_per_group : 1;
+    const int64_t pages = std::max(1, (prm.max_context_len + kPageRows - 1) / kPageRows);
+    if (prm.B > kBalMaxBatch || (int64_t)prm.B * prm.Hkv * groups > INT32_MAX / pages) return PKV_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const StreamWorkspace w = stream_workspace(sms, tiles);
+    if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PKV_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    prm.ws_count = reinterpret_cast<unsigned int*>(ws + w.tickets);
+    prm.ws_ml = reinterpret_cast<float4*>(ws + w.ml);
+    prm.ws_o = reinterpret_cast<float4*>(ws + w.o);
+    CUtensorMap mk, mv, ms;
+    if (!cached_cache_map(&mk, k_cache, true, prm.num_blocks, prm.Hkv) ||
+        !cached_cache_map(&mv, v_cache, true, prm.num_blocks, prm.Hkv) ||
+        !cached_scale_map(&ms, kv_scales, prm.num_blocks, prm.Hkv))
+        return PKV_ERR_CUDA;
+    switch (tiles) {
+        case 1: return launch_stream_int8<1>(prm, mk, mv, ms, sms, st);
+        case 2: return launch_stream_int8<2>(prm, mk, mv, ms, sms, st);
+        case 3: return launch_stream_int8<3>(prm, mk, mv, ms, sms, st);
+        default: return launch_stream_int8<4>(prm, mk, mv, ms, sms, st);
+    }
+}
+
+// Arguments shared by the cache write with rotation (or without: half = 0) and
+// the cache read. The 8-bit cache keeps its scales per 16-row page.
+pkv_status check_cache_rows(const void* k_cache, const void* v_cache, const float* kv_scales,
+                            const int64_t* slot_mapping, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t num_blocks, int32_t block_size, int32_t kv_dtype, float k_scale, float v_scale) {
+    if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || block_size <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (kv_dtype != PKV_KV_F16 && kv_dtype != PKV_KV_FP8_E4M3 && kv_dtype != PKV_KV_INT8) return PKV_ERR_INVALID_ARG;
+    if (kv_dtype == PKV_KV_FP8_E4M3 &&
+        !(k_scale > 0.f && v_scale > 0.f && std::isfinite(k_scale) && std::isfinite(v_scale)))
+        return PKV_ERR_INVALID_ARG;
+    if (head_dim != kHeadDim || (kv_dtype == PKV_KV_INT8 && block_size != kPageRows)) return PKV_ERR_UNSUPPORTED;
+    if (num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !slot_mapping || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PKV_ERR_INVALID_ARG;
+    if (kv_dtype == PKV_KV_INT8 && (!kv_scales || !aligned16(kv_scales))) return PKV_ERR_INVALID_ARG;
+    return PKV_OK;
+}
+
+// Launches the write for a checked call. One block of up to 512 threads takes
+// whole tokens, eight threads to a head row: enough tokens for 256 threads.
+pkv_status launch_rope_write(pkv::RopeWriteParams& prm, int32_t kv_dtype, cudaStream_t st) {
+    const int rows = prm.Hq + 2 * prm.Hkv;
+    prm.tokens_per_block = std::max(1, std::min(32, 32 / rows));
+    const int64_t want = (int64_t)prm.tokens_per_block * rows * 8;
+    const int threads = (int)std::min<int64_t>(512, (want + 31) / 32 * 32);
+    const unsigned blocks = (unsigned)((prm.num_tokens + prm.tokens_per_block - 1) / prm.tokens_per_block);
+    const size_t smem = (size_t)prm.tokens_per_block * prm.half * sizeof(float2);
+    cudaError_t e;
+    switch (kv_dtype) {
+        case PKV_KV_F16: e = launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheF16>, dim3(blocks), dim3(threads), smem, st, prm); break;
+        case PKV_KV_FP8_E4M3: e = launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheFp8>, dim3(blocks), dim3(threads), smem, st, prm); break;
+        default: e = launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheInt8>, dim3(blocks), dim3(threads), smem, st, prm);
+    }
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status rope_write_impl(void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache,
+                           void* v_cache, float* kv_scales, const int64_t* slot_mapping, const int64_t* positions,
+                           const float* inv_freq, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t rotary_dim, int32_t num_axes, const int32_t* axis_sections,
+                           int32_t num_blocks, int32_t block_size, int32_t kv_dtype, float k_scale, float v_scale,
+                           const DeviceScales& ds, uint32_t flags, void* stream) {
+    if (flags & ~(PKV_ROPE_INTERLEAVED | PKV_ROPE_CYCLIC_AXES)) return PKV_ERR_INVALID_ARG;
+    if (num_q_heads < 0 || rotary_dim <= 0 || rotary_dim > head_dim || rotary_dim % 2 || num_axes <= 0 ||
+        !axis_sections)
+        return PKV_ERR_INVALID_ARG;
+    if (num_axes > pkv::kRopeMaxAxes || rotary_dim % 16 || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    const int half = rotary_dim / 2;
+    const bool cyclic = (flags & PKV_ROPE_CYCLIC_AXES) != 0;
+    int64_t sum = 0;
+    for (int a = 0; a < num_axes; ++a) {
+        if (axis_sections[a] < 0 || axis_sections[a] > half) return PKV_ERR_INVALID_ARG;
+        sum += axis_sections[a];
+        // axis a's last frequency under the cyclic order lies inside the rotated part
+        if (cyclic && a > 0 && axis_sections[a] > 0 && num_axes * (axis_sections[a] - 1) + a >= half)
+            return PKV_ERR_INVALID_ARG;
+    }
+    if (sum != half) return PKV_ERR_INVALID_ARG;
+    const pkv_status v = check_cache_rows(k_cache, v_cache, kv_scales, slot_mapping, num_tokens, num_kv_heads, head_dim,
+                                          num_blocks, block_size, kv_dtype, k_scale, v_scale);
+    if (v != PKV_OK || num_tokens == 0) return v;
+    if (!k_new || !v_new || !positions || !inv_freq || (num_q_heads > 0 && (!q || !q_out))) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(q_out) ||
+        (reinterpret_cast<uintptr_t>(positions) & 7u) || (reinterpret_cast<uintptr_t>(inv_freq) & 3u))
+        return PKV_ERR_INVALID_ARG;
+    // q may be rotated in place; any other overlap of what is read and written is an error
+    const int64_t qb = (int64_t)num_tokens * num_q_heads * head_dim * 2, kb = (int64_t)num_tokens * num_kv_heads * head_dim * 2;
+    if ((q != q_out && ranges_overlap(q, qb, q_out, qb)) || ranges_overlap(k_new, kb, q_out, qb) ||
+        ranges_overlap(v_new, kb, q_out, qb))
+        return PKV_ERR_INVALID_ARG;
+    pkv::RopeWriteParams prm{};
+    prm.q_out = static_cast<__half*>(q_out);
+    prm.q = static_cast<const __half*>(q);
+    prm.k_new = static_cast<const __half*>(k_new);
+    prm.v_new = static_cast<const __half*>(v_new);
+    prm.k_cache = k_cache;
+    prm.v_cache = v_cache;
+    prm.kv_scales = kv_scales;
+    prm.slot_mapping = slot_mapping;
+    prm.positions = positions;
+    prm.inv_freq = inv_freq;
+    prm.num_slots = (int64_t)num_blocks * block_size;
+    prm.num_tokens = num_tokens;
+    prm.Hq = num_q_heads;
+    prm.Hkv = num_kv_heads;
+    prm.half = half;
+    prm.axes = num_axes;
+    prm.cyclic = cyclic ? 1 : 0;
+    prm.pairs = (flags & PKV_ROPE_INTERLEAVED) ? 1 : 0;
+    for (int a = 0; a < num_axes; ++a) prm.sections[a] = axis_sections[a];
+    prm.k_scale = k_scale;
+    prm.v_scale = v_scale;
+    prm.k_scales = ds.k;
+    prm.v_scales = ds.v;
+    prm.scales_per_head = ds.per_head;
+    return launch_rope_write(prm, kv_dtype, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -965,9 +1185,14 @@ pkv_status paged_gqa_decode_step_fp8_scaled(
 size_t paged_gqa_prefill_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                         int32_t kv_dtype) {
     if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim != kHeadDim || num_q_heads % num_kv_heads != 0 ||
-        num_q_heads / num_kv_heads > pkv::kGroupPad || (kv_dtype != PKV_KV_F16 && kv_dtype != PKV_KV_FP8_E4M3))
+        num_q_heads / num_kv_heads > pkv::kGroupPad ||
+        (kv_dtype != PKV_KV_F16 && kv_dtype != PKV_KV_FP8_E4M3 && kv_dtype != PKV_KV_INT8))
         return 0;
     if (kv_dtype == PKV_KV_FP8_E4M3) return 0;                  // the warp-level FP8 kernel takes none
+    if (kv_dtype == PKV_KV_INT8) {
+        const int n = device_sms();
+        return n > 0 ? std::max(stream_workspace(n, 1).total, stream_workspace(n, kStreamMaxTiles).total) : 0;
+    }
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
@@ -1094,6 +1319,156 @@ pkv_status fused_add_rmsnorm_qkv(const void* x, const void* residual, const void
     prm.eps = eps;
     prm.prefetch_w = (flags & PKV_STEP_OVERLAP_PREVIOUS) ? 1 : 0;
     return launch_qkv(pl, prm, w_qkv, x, residual, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_kv_cache_write_int8(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                                     float* kv_scales, const int64_t* slot_mapping, int32_t num_tokens,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
+                                     void* stream) {
+    const pkv_status v = check_cache_rows(k_cache, v_cache, kv_scales, slot_mapping, num_tokens, num_kv_heads, head_dim,
+                                          num_blocks, block_size, PKV_KV_INT8, 1.f, 1.f);
+    if (v != PKV_OK || num_tokens == 0) return v;
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return PKV_ERR_INVALID_ARG;
+    pkv::RopeWriteParams prm{};                      // no q heads, nothing rotated
+    prm.k_new = static_cast<const __half*>(k_new);
+    prm.v_new = static_cast<const __half*>(v_new);
+    prm.k_cache = k_cache;
+    prm.v_cache = v_cache;
+    prm.kv_scales = kv_scales;
+    prm.slot_mapping = slot_mapping;
+    prm.num_slots = (int64_t)num_blocks * block_size;
+    prm.num_tokens = num_tokens;
+    prm.Hkv = num_kv_heads;
+    prm.axes = 1;
+    return launch_rope_write(prm, PKV_KV_INT8, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_kv_rope_cache_write(void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                     void* v_cache, float* kv_scales, const int64_t* slot_mapping,
+                                     const int64_t* positions, const float* inv_freq, int32_t num_tokens,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                                     int32_t num_axes, const int32_t* axis_sections, int32_t num_blocks,
+                                     int32_t block_size, int32_t kv_dtype, float k_scale, float v_scale,
+                                     uint32_t flags, void* stream) {
+    return rope_write_impl(q_out, q, k_new, v_new, k_cache, v_cache, kv_scales, slot_mapping, positions, inv_freq,
+                           num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, num_axes, axis_sections,
+                           num_blocks, block_size, kv_dtype, k_scale, v_scale, DeviceScales{}, flags, stream);
+}
+
+pkv_status paged_kv_rope_cache_write_fp8_scaled(
+    void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+    const int64_t* slot_mapping, const int64_t* positions, const float* inv_freq, int32_t num_tokens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim, int32_t num_axes,
+    const int32_t* axis_sections, int32_t num_blocks, int32_t block_size, const float* k_scales,
+    const float* v_scales, int32_t scales_per_head, uint32_t flags, void* stream) {
+    const pkv_status v = check_device_scales(k_scales, v_scales, scales_per_head);
+    if (v != PKV_OK) return v;
+    return rope_write_impl(q_out, q, k_new, v_new, k_cache, v_cache, nullptr, slot_mapping, positions, inv_freq,
+                           num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, num_axes, axis_sections,
+                           num_blocks, block_size, PKV_KV_FP8_E4M3, 1.f, 1.f,
+                           DeviceScales{k_scales, v_scales, scales_per_head}, flags, stream);
+}
+
+pkv_status paged_kv_cache_read(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const float* kv_scales, const int64_t* slot_mapping, int32_t num_tokens,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
+                               int32_t kv_dtype, float k_scale, float v_scale, void* stream) {
+    const pkv_status v = check_cache_rows(k_cache, v_cache, kv_scales, slot_mapping, num_tokens, num_kv_heads, head_dim,
+                                          num_blocks, block_size, kv_dtype, k_scale, v_scale);
+    if (v != PKV_OK || num_tokens == 0) return v;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return PKV_ERR_INVALID_ARG;
+    pkv::CacheReadParams prm{};
+    prm.k_out = static_cast<__half*>(k_out);
+    prm.v_out = static_cast<__half*>(v_out);
+    prm.k_cache = k_cache;
+    prm.v_cache = v_cache;
+    prm.kv_scales = kv_scales;
+    prm.slot_mapping = slot_mapping;
+    prm.num_slots = (int64_t)num_blocks * block_size;
+    prm.num_tokens = num_tokens;
+    prm.Hkv = num_kv_heads;
+    prm.k_scale = k_scale;
+    prm.v_scale = v_scale;
+    const int64_t blocks = ((int64_t)num_tokens * 2 * num_kv_heads + 31) / 32;   // 32 head rows a block
+    if (blocks > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 g((unsigned)blocks), t(256);
+    const cudaError_t e =
+        kv_dtype == PKV_KV_F16        ? launch_pdl(pkv::cache_read_kernel<pkv::kCacheF16>, g, t, 0, st, prm)
+        : kv_dtype == PKV_KV_FP8_E4M3 ? launch_pdl(pkv::cache_read_kernel<pkv::kCacheFp8>, g, t, 0, st, prm)
+                                      : launch_pdl(pkv::cache_read_kernel<pkv::kCacheInt8>, g, t, 0, st, prm);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+size_t paged_gqa_decode_workspace_size_int8(void) {
+    const int sms = device_sms();
+    return sms > 0 ? stream_workspace(sms, 1).total : 0;
+}
+
+pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                           const float* kv_scales, const int32_t* block_tables,
+                                           const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                           int32_t max_blocks_per_seq, int32_t num_blocks, int32_t max_context_len,
+                                           float softmax_scale, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+    const pkv_status v = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, batch, num_q_heads,
+                                              num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                                              max_context_len, softmax_scale, PKV_KV_F16, 1.f, 1.f, 0);
+    if (v != PKV_OK || batch == 0) return v;
+    if (!kv_scales || !aligned16(kv_scales)) return PKV_ERR_INVALID_ARG;
+    pkv::StreamInt8Params prm{};
+    prm.out = static_cast<__half*>(out);
+    prm.q = static_cast<const __half*>(q);
+    prm.block_tables = block_tables;
+    prm.context_lens = context_lens;
+    prm.B = batch;
+    prm.Hq = num_q_heads;
+    prm.Hkv = num_kv_heads;
+    prm.G = num_q_heads / num_kv_heads;
+    prm.total = batch;
+    prm.max_query_len = 1;
+    prm.max_blocks_per_seq = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.max_context_len = max_context_len;
+    prm.logit_scale_log2 = softmax_scale * 1.4426950408889634f;
+    return stream_int8(prm, k_cache, v_cache, kv_scales, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                            const float* kv_scales, const int32_t* block_tables,
+                                            const int32_t* context_lens, const int32_t* query_start, int32_t batch,
+                                            int32_t total_queries, int32_t max_query_len, int32_t num_q_heads,
+                                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                            int32_t max_blocks_per_seq, int32_t num_blocks, int32_t max_context_len,
+                                            float softmax_scale, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+    if (total_queries < 0 || max_query_len < 0) return PKV_ERR_INVALID_ARG;
+    const bool any = batch > 0 && total_queries > 0 && max_query_len > 0;
+    const pkv_status v = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, any ? batch : std::min(batch, 0),
+                                              num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                                              num_blocks, max_context_len, softmax_scale, PKV_KV_F16, 1.f, 1.f, 0);
+    if (v != PKV_OK || !any) return v;
+    if (!kv_scales || !aligned16(kv_scales)) return PKV_ERR_INVALID_ARG;
+    if (!query_start || (reinterpret_cast<uintptr_t>(query_start) & 3u)) return PKV_ERR_INVALID_ARG;
+    if (max_query_len > max_context_len) return PKV_ERR_INVALID_ARG;
+    pkv::StreamInt8Params prm{};
+    prm.out = static_cast<__half*>(out);
+    prm.q = static_cast<const __half*>(q);
+    prm.block_tables = block_tables;
+    prm.context_lens = context_lens;
+    prm.query_start = query_start;
+    prm.B = batch;
+    prm.Hq = num_q_heads;
+    prm.Hkv = num_kv_heads;
+    prm.G = num_q_heads / num_kv_heads;
+    prm.total = total_queries;
+    prm.max_query_len = max_query_len;
+    prm.max_blocks_per_seq = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.max_context_len = max_context_len;
+    prm.logit_scale_log2 = softmax_scale * 1.4426950408889634f;
+    return stream_int8(prm, k_cache, v_cache, kv_scales, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,648 @@
+// Attention over the 8-bit paged cache with a scale per token and KV head
+// (int8_cache.cuh), load-balanced streaming form: decode (one query token per
+// sequence) and short chunks of new tokens.
+//
+// Work is cut as in decode_balanced.cuh: a unit is one page (16 tokens) of one
+// KV head of one sequence, for one group of query tokens; the units of the
+// batch form a row, every warp of the persistent grid takes an equal run of
+// it, streams its pages through its own ring of TMA copies, and the pieces of
+// a segment that was cut between warps are merged by a fan-in-32 ticket tree.
+// Nothing waits on another CTA.
+//
+// Columns: the N side of the tensor-core products (mma.sync m16n8k16, tokens
+// on M) holds NT tiles of 8 columns, column = (query token, head of the KV
+// head's group), floor(8 NT / G) query tokens to a group. Decode has NT = 1
+// and one query. With more columns a page is converted to f16 once and serves
+// all of them. Each column has its own causal limit.
+//
+// The mathematics, for a column with query vector q and a token t with codes
+// ck_t, cv_t (exact in f16) and scales ks_t, vs_t:
+//   x_t = softmax_scale log2(e) ks_t (q . ck_t)        logit, exp2 domain
+//   y_t = x_t + log2(vs_t),  w_t = 2^(y_t - m)         weight of cv_t
+//   O = sum w_t cv_t,  l = sum w_t / vs_t,  out = O / l
+// Moving the value scale into the exponent keeps the weights that are rounded
+// to f16 for the tensor cores (2^-12 each) in [0, 64] whatever the scales
+// are, and leaves the codes exact; l is summed in fp32 from the unrounded
+// weights. m follows the largest y only when that exceeds it by more than 6
+// (so w <= 64): most pages then skip the rescaling of O and l.
+// Codes are finite, so rows past the context need no zeroing: their weight is
+// 0. A scale outside [0, 2^60] is flagged and counts as 0, a row of zeros
+// (V: 2^-60 in its place, which rounds to zeros in any f16 output).
+//
+// Bound: HBM. Bytes of a unit: 2 x 16 x (128 + 4).
+#pragma once
+
+#include <type_traits>
+
+#include "decode_balanced.cuh"
+#include "int8_cache.cuh"
+
+namespace pkv {
+
+struct StreamInt8Params {
+    __half* out;                  // [B, Hq, 128], or [total, Hq, 128] with query_start
+    const __half* q;
+    const int32_t* block_tables;  // [B, max_blocks_per_seq]
+    const int32_t* context_lens;  // [B]
+    const int32_t* query_start;   // [B + 1], or null: one query per sequence (decode)
+    float4* ws_o;                 // [2 * workers][NT][8][32 lanes]  pieces' unnormalised O
+    float4* ws_ml;                // [2 * workers][NT][4]  (m, l) of columns 2c, 2c + 1
+    unsigned int* ws_count;       // tickets of the merge tree, zero between calls
+    int32_t B, Hq, Hkv, G;
+    int32_t total, max_query_len;
+    int32_t max_blocks_per_seq, num_blocks, max_context_len;
+    int32_t queries_per_group;    // floor(8 NT / G), 1 in decode
+    int32_t min_units_per_worker;
+    float logit_scale_log2;       // softmax_scale * log2(e)
+};
+
+constexpr float kScaleMax = 1.152921504606846976e18f;      // 2^60
+constexpr float kScaleMin = 8.673617379884035472e-19f;     // 2^-60
+constexpr float kStreamRaise = 6.f;                        // log2 of the largest weight
+constexpr float kLogitFloor = -1e30f;                      // stands in for a maximum of -inf
+
+template <int kNT, int kWarps, int kStages>
+struct StreamInt8Shape {
+    static constexpr int kTileBytes = 2048;                 // one page of K (or V) codes, one head
+    static constexpr int kSlotBytes = 2 * kTileBytes;
+    static constexpr int kScaleBytes = 128;                 // K scales, V scales of the page
+    static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
+    static constexpr int kScaleRing = kWarps * kStages * kScaleBytes;
+    static constexpr bool kQShared = kNT > 1;               // query fragments in shared memory
+    static constexpr int kQBytes = kQShared ? kWarps * kNT * 8 * 32 * 8 : 0;
+    static constexpr int kMergeBytes = kWarps * kMergeFloats * 4;
+    static constexpr int kBarBytes = kWarps * kStages * 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kFixed = 1024 + kRingBytes + kScaleRing + kQBytes + kMergeBytes + kBarBytes;
+    static size_t smem_bytes(int B) { return (size_t)kFixed + ((size_t)(B + 1) * 4 + 15) / 16 * 16; }
+};
+
+// Four codes (low byte first) to two f16x2 of their exact values: 0x6400 | code
+// is 1024 + code in f16, and 1152 is subtracted exactly.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t h) {
+    const uint32_t bias = 0x64806480u;
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+// bytes (0, 1) and (2, 3): consecutive channels of one token
+__device__ __forceinline__ void codes_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    lo = sub_1152(prmt(w, 0x64646464u, 0x5140u));
+    hi = sub_1152(prmt(w, 0x64646464u, 0x5342u));
+}
+// bytes (0, 2) and (1, 3): one channel of two tokens each
+__device__ __forceinline__ void codes_to_half2x2_cross(uint32_t w, uint32_t& even, uint32_t& odd) {
+    even = sub_1152(prmt(w, 0x64646464u, 0x5240u));
+    odd = sub_1152(prmt(w, 0x64646464u, 0x5341u));
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lds32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+template <int kNT, int kWarps, int kStages>
+__global__ void __launch_bounds__(32 * kWarps)
+stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_s, const StreamInt8Params p) {
+    using S = StreamInt8Shape<kNT, kWarps, kStages>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_warp_sum[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = p.B, Hkv = p.Hkv, G = p.G;
+    const bool chunked = p.query_start != nullptr;
+
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t ring = (raw + 1023u) & ~1023u;
+    const uint32_t scale_ring = ring + S::kRingBytes;
+    const uint32_t q_smem = scale_ring + S::kScaleRing;
+    uint8_t* after = smem_raw + (ring - raw) + S::kRingBytes + S::kScaleRing + S::kQBytes;
+    float* wts = reinterpret_cast<float*>(after) + warp * kMergeFloats;    // [32 items][8 columns], M[8], L[8]
+    const uint32_t bars = q_smem + S::kQBytes + S::kMergeBytes;
+    int* prefix = reinterpret_cast<int*>(after + S::kMergeBytes + S::kBarBytes);   // [B + 1]
+
+    grid_dependency_wait();                       // inputs may come from the previous launch
+    grid_dependents_launch();
+
+    const int cap = min(p.max_context_len, p.max_blocks_per_seq * kPageRows);
+    const int qpg = p.queries_per_group;
+    // context length and query count of sequence b (decode: clamped, one query; chunk: inconsistent
+    // lengths give no queries); `flag`: report what was wrong
+    auto sequence = [&](int b, int& L, int& nq, bool flag) {
+        L = __ldg(p.context_lens + b);
+        if (!chunked) {
+            nq = 1;
+            if (L < 0 || L > cap) {
+                if (flag) flag_error(PKV_DEVERR_CONTEXT_LEN);
+                L = L < 0 ? 0 : cap;
+            }
+            return;
+        }
+        const int q0 = __ldg(p.query_start + b), q1 = __ldg(p.query_start + b + 1);
+        nq = q1 - q0;
+        if (q0 < 0 || q1 < q0 || q1 > p.total || nq > p.max_query_len || L < nq || L > cap) {
+            if (flag) flag_error(PKV_DEVERR_CONTEXT_LEN);
+            nq = 0;
+        }
+    };
+    auto units_of_seq = [&](int b, bool flag) -> int {
+        int L, nq;
+        sequence(b, L, nq, flag);
+        return Hkv * ((nq + qpg - 1) / qpg) * ((L + kPageRows - 1) / kPageRows);
+    };
+
+    // ---- unit order: units of sequence b start at prefix[b], as (KV head, query group, page) ----
+    {
+        const int per = (B + S::kThreads - 1) / S::kThreads;
+        const int b_lo = min(B, (int)threadIdx.x * per), b_hi = min(B, b_lo + per);
+        int local = 0;
+        for (int b = b_lo; b < b_hi; ++b) local += units_of_seq(b, blockIdx.x == 0);
+        int incl = local;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        if (lane == 31) s_warp_sum[warp] = incl;
+        if (lane == 0)
+            for (int s = 0; s < kStages; ++s) mbar_init(bars + 8u * (warp * kStages + s), 1);
+        mbar_init_fence();
+        __syncthreads();
+        int run = incl - local;
+        for (int w = 0; w < warp; ++w) run += s_warp_sum[w];
+        for (int b = b_lo; b < b_hi; ++b) {
+            prefix[b] = run;
+            run += units_of_seq(b, false);
+        }
+        if (b_hi == B && b_lo < B) prefix[B] = run;
+        __syncthreads();
+    }
+    const int U = prefix[B];
+    const int W_total = gridDim.x * kWarps;
+    const int worker = blockIdx.x * kWarps + warp;
+    // decode: empty contexts get zero rows, spread over all warps
+    if (!chunked) {
+        for (int b = worker; b < B; b += W_total) {
+            if (prefix[b + 1] != prefix[b]) continue;
+            uint4* ob = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.Hq * kHeadDim);
+            for (int i = lane; i < p.Hq * kHeadDim / 8; i += 32) ob[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    const int want = (int)(((int64_t)U + p.min_units_per_worker - 1) / p.min_units_per_worker);
+    const int W = min(W_total, max(1, want));
+    const int u0 = U == 0 ? 0 : (int)range_start(worker, U, W);
+    const int n = (U == 0 || worker >= W) ? 0 : (int)range_start(worker + 1, U, W) - u0;
+    if (n <= 0) return;
+    if (lane == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_s);
+    }
+
+    auto full_bar = [&](int s) { return bars + 8u * (warp * kStages + s); };
+    auto k_tile = [&](int s) { return ring + (warp * kStages + s) * S::kSlotBytes; };
+    auto s_tile = [&](int s) { return scale_ring + (warp * kStages + s) * S::kScaleBytes; };
+    auto pages_of = [&](int b) { return (min(max(__ldg(p.context_lens + b), 0), cap) + kPageRows - 1) / kPageRows; };
+
+    // Block-table window: lane k holds (physical block, KV head) of unit 32 w + k.
+    auto load_window = [&](int w, int& phys, int& head) {
+        const int t = 32 * w + lane;
+        phys = -1;
+        head = 0;
+        if (t < n) {
+            const int u = u0 + t;
+            const int b = seq_of_unit(prefix, B, u);
+            const int nb = pages_of(b);
+            const int rr = u - prefix[b];
+            const int seg = rr / nb;                            // (KV head, query group)
+            head = seg / ((prefix[b + 1] - prefix[b]) / nb / Hkv);
+            phys = __ldg(p.block_tables + (int64_t)b * p.max_blocks_per_seq + (rr - seg * nb));
+        }
+    };
+    int win_phys, win_head, nxt_phys, nxt_head, cur_win = 0;
+    load_window(0, win_phys, win_head);
+    load_window(1, nxt_phys, nxt_head);
+    // a page is read once, unless several query groups of a sequence read it
+    const uint64_t policy = chunked && p.max_query_len > qpg ? l2_evict_normal_policy() : l2_evict_first_policy();
+    int issued = 0;                              // units [0, issued) have their copies in flight or landed
+    auto issue = [&](int t) {
+        const int w = t >> 5;
+        if (w != cur_win) {                      // windows are consumed in order
+            win_phys = nxt_phys;
+            win_head = nxt_head;
+            cur_win = w;
+            load_window(w + 1, nxt_phys, nxt_head);
+        }
+        int pb = __shfl_sync(0xffffffffu, win_phys, t & 31);
+        const int hg = __shfl_sync(0xffffffffu, win_head, t & 31);
+        issued = t + 1;
+        if (lane == 0) {
+            if (pb < 0 || pb >= p.num_blocks) {  // outside the pool: scales (and codes) read as zeros
+                flag_error(PKV_DEVERR_BLOCK_ID);
+                pb = -1;
+            }
+            const int s = t % kStages;
+            fence_proxy_async_shared();          // earlier generic reads of the slot come first
+            mbar_arrive_expect_tx(full_bar(s), S::kSlotBytes + S::kScaleBytes);
+            tma_load_3d(s_tile(s), &tm_s, full_bar(s), 0, hg, pb, policy);
+            tma_load_3d(k_tile(s), &tm_k, full_bar(s), 0, hg, pb * kPageRows, policy);
+            tma_load_3d(k_tile(s) + S::kTileBytes, &tm_v, full_bar(s), 0, hg, pb * kPageRows, policy);
+        }
+    };
+    for (int t = 0; t < min(n, kStages); ++t) issue(t);
+
+    // ---- the current segment: sequence b, KV head g, query group grp; page j of nb ----
+    const int r = lane >> 2, c = lane & 3;
+    int b = seq_of_unit(prefix, B, u0);
+    int nb = pages_of(b);
+    int seg = (u0 - prefix[b]) / nb;
+    int j = (u0 - prefix[b]) - seg * nb;
+    int piece_j0 = j;
+    int g = 0, row0 = 0, ncols = 0;              // first row of q/out of the group, live columns
+    int lim_lo = 0, lim_hi = 0;                  // positions of the group's first and last query
+    int lim[kNT][2];                             // causal limits of this lane's columns 2c, 2c + 1
+    uint32_t qreg[S::kQShared ? 1 : 8][2];
+    auto open_segment = [&]() {
+        int L, nq;
+        sequence(b, L, nq, false);
+        const int ngroups = (nq + qpg - 1) / qpg;
+        g = seg / ngroups;
+        const int i0 = (seg - g * ngroups) * qpg;               // first query of the group
+        const int cnt = min(qpg, nq - i0);
+        row0 = (chunked ? __ldg(p.query_start + b) : b) + i0;
+        ncols = cnt * G;
+        lim_lo = L - nq + i0;
+        lim_hi = lim_lo + cnt - 1;
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = 8 * t + 2 * c + e;
+                lim[t][e] = col < ncols ? lim_lo + col / G : lim_hi;   // idle columns follow the last query
+            }
+            // the query vector of column 8 t + r, as the B operand: channels 16 kk + 4c .. + 3
+            const int col = 8 * t + r;
+            const uint2* qrow = reinterpret_cast<const uint2*>(
+                p.q + ((int64_t)(row0 + col / G) * p.Hq + (int64_t)g * G + col % G) * kHeadDim);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                const uint2 v = col < ncols ? __ldg(qrow + 4 * kk + c) : make_uint2(0u, 0u);
+                if constexpr (S::kQShared) {
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};"
+                                 :: "r"(q_smem + (((warp * kNT + t) * 8 + kk) * 32 + lane) * 8), "r"(v.x), "r"(v.y)
+                                 : "memory");
+                } else {
+                    qreg[kk][0] = v.x;
+                    qreg[kk][1] = v.y;
+                }
+            }
+        }
+    };
+    auto q_frag = [&](int t, int kk, uint32_t& b0, uint32_t& b1) {
+        if constexpr (S::kQShared) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(b0), "=r"(b1)
+                         : "r"(q_smem + (((warp * kNT + t) * 8 + kk) * 32 + lane) * 8));
+        } else {
+            b0 = qreg[kk][0];
+            b1 = qreg[kk][1];
+        }
+    };
+    open_segment();
+
+    float m[kNT][2], l[kNT][2], o[kNT][8][4];
+    auto reset = [&]() {
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+        }
+    };
+    reset();
+    const float sl = p.logit_scale_log2;
+
+    // One online-softmax step over kPages consecutive pages (slots s0, s1) from page jp on.
+    auto attend = [&](auto pages_tag, int s0, int s1, int jp) {
+        constexpr int kPages = decltype(pages_tag)::value;
+        float x[kPages][kNT][4], lv[kPages][2], rv[kPages][2];
+#pragma unroll
+        for (int pg = 0; pg < kPages; ++pg) {
+            const int s = pg ? s1 : s0;
+            const uint32_t kt = k_tile(s), sc = s_tile(s);
+            float ks[2];
+            const int t0 = (jp + pg) * kPageRows;               // position of the page's first token
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float kr = lds32(sc + 4 * (r + 8 * e)), vr = lds32(sc + 64 + 4 * (r + 8 * e));
+                const bool k_ok = kr >= 0.f && kr <= kScaleMax, v_ok = vr >= 0.f && vr <= kScaleMax;
+                if (t0 + r + 8 * e <= lim_hi && !(k_ok && v_ok)) flag_error(PKV_DEVERR_SCALE);
+                ks[e] = k_ok ? kr * sl : 0.f;
+                const float v = v_ok ? fmaxf(vr, kScaleMin) : kScaleMin;
+                lv[pg][e] = fast_log2(v);
+                rv[pg][e] = fast_rcp(v);
+            }
+            // S^T (16 tokens x 8 columns) = K (16 x 128) . Q^T, in the codes' units. A single column
+            // tile keeps two accumulators, to halve its chain of dependent products.
+            constexpr int kAcc = kNT == 1 ? 2 : 1;
+            float acc[kNT][kAcc][4];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int a = 0; a < kAcc; ++a) acc[t][a][0] = acc[t][a][1] = acc[t][a][2] = acc[t][a][3] = 0.f;
+            const int row = lane & 15;
+#pragma unroll
+            for (int J = 0; J < 4; ++J) {
+                const int chunk = 2 * J + (lane >> 4);
+                uint32_t w0, w1, w2, w3;                        // 4 codes each: channels 16 chunk + 4c .. + 3
+                ldsm_x4(kt + row * 128 + ((chunk ^ (row & 7)) << 4), w0, w1, w2, w3);
+                uint32_t h[8];
+                codes_to_half2x2(w0, h[0], h[1]);
+                codes_to_half2x2(w1, h[2], h[3]);
+                codes_to_half2x2(w2, h[4], h[5]);
+                codes_to_half2x2(w3, h[6], h[7]);
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) {
+                    uint32_t b0, b1;
+                    q_frag(t, 2 * J, b0, b1);
+                    mma_16816(acc[t][0], h[0], h[2], h[1], h[3], b0, b1);
+                    q_frag(t, 2 * J + 1, b0, b1);
+                    mma_16816(acc[t][kAcc - 1], h[4], h[6], h[5], h[7], b0, b1);
+                }
+            }
+            const bool whole = t0 + kPageRows - 1 <= lim_lo;    // every row live for every column
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s_raw = acc[t][0][e];
+                    if constexpr (kAcc == 2) s_raw += acc[t][1][e];
+                    float y = fmaf(s_raw, ks[e >> 1], lv[pg][e >> 1]);
+                    if (!whole && t0 + r + 8 * (e >> 1) > lim[t][e & 1]) y = -INFINITY;
+                    x[pg][t][e] = y;
+                }
+        }
+        uint32_t pb[kPages][kNT][2];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+            for (int pg = 0; pg < kPages; ++pg) {
+                b0 = fmaxf(b0, fmaxf(x[pg][t][0], x[pg][t][2]));
+                b1 = fmaxf(b1, fmaxf(x[pg][t][1], x[pg][t][3]));
+            }
+            if (__any_sync(0xffffffffu, b0 > m[t][0] + kStreamRaise || b1 > m[t][1] + kStreamRaise)) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, off));
+                    b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, off));
+                }
+                const float n0 = fmaxf(m[t][0], b0), n1 = fmaxf(m[t][1], b1);
+                // (a column that has seen no live row keeps m = -inf, l = 0 and O = 0)
+                const float a0 = fast_exp2(m[t][0] - fmaxf(n0, kLogitFloor));
+                const float a1 = fast_exp2(m[t][1] - fmaxf(n1, kLogitFloor));
+                m[t][0] = n0;
+                m[t][1] = n1;
+                l[t][0] *= a0;
+                l[t][1] *= a1;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[t][i][0] *= a0; o[t][i][1] *= a1; o[t][i][2] *= a0; o[t][i][3] *= a1;
+                }
+            }
+            const float m0 = fmaxf(m[t][0], kLogitFloor), m1 = fmaxf(m[t][1], kLogitFloor);
+#pragma unroll
+            for (int pg = 0; pg < kPages; ++pg) {
+                const float p0 = fast_exp2(x[pg][t][0] - m0), p1 = fast_exp2(x[pg][t][1] - m1);
+                const float p2 = fast_exp2(x[pg][t][2] - m0), p3 = fast_exp2(x[pg][t][3] - m1);
+                l[t][0] = fmaf(p0, rv[pg][0], fmaf(p2, rv[pg][1], l[t][0]));
+                l[t][1] = fmaf(p1, rv[pg][0], fmaf(p3, rv[pg][1], l[t][1]));
+                // P^T as the B operand: transpose the (token x column) accumulator layout
+                pb[pg][t][0] = movmatrix_trans(pack_half2(p0, p1));
+                pb[pg][t][1] = movmatrix_trans(pack_half2(p2, p3));
+            }
+        }
+        // O^T (128 channels x 8 columns) += V^T . P^T: a transposing load of byte pairs gives lane
+        // (r, c) channels 16 i + 2r, + 1 of tokens 2c, 2c + 1, so rows r and r + 8 of product tile i
+        // are channels 16 i + 2r and 16 i + 2r + 1
+#pragma unroll
+        for (int pg = 0; pg < kPages; ++pg) {
+            const uint32_t vt = k_tile(pg ? s1 : s0) + S::kTileBytes;
+            const int row = lane & 15;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const int chunk = i + (lane >> 4);
+                uint32_t w0, w1, w2, w3;
+                ldsm_x4_trans(vt + row * 128 + ((chunk ^ (row & 7)) << 4), w0, w1, w2, w3);
+                uint32_t h[8];
+                codes_to_half2x2_cross(w0, h[0], h[1]);
+                codes_to_half2x2_cross(w1, h[2], h[3]);
+                codes_to_half2x2_cross(w2, h[4], h[5]);
+                codes_to_half2x2_cross(w3, h[6], h[7]);
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) {
+                    mma_16816(o[t][i], h[0], h[1], h[2], h[3], pb[pg][t][0], pb[pg][t][1]);
+                    mma_16816(o[t][i + 1], h[4], h[5], h[6], h[7], pb[pg][t][0], pb[pg][t][1]);
+                }
+            }
+        }
+    };
+
+    // out[row, head of g] of column tile t, from fragment-order values times inv0, inv1
+    auto write_out = [&](int t, const float (&v)[8][4], float inv0, float inv1) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int col = 8 * t + 2 * c + e;
+            if (col >= ncols) continue;
+            __half2* dst = reinterpret_cast<__half2*>(
+                p.out + ((int64_t)(row0 + col / G) * p.Hq + (int64_t)g * G + col % G) * kHeadDim);
+            const float inv = e ? inv1 : inv0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[8 * i + r] = __floats2half2_rn(v[i][e] * inv, v[i][2 + e] * inv);
+        }
+    };
+    auto store_item = [&](int slot, int t, const float (&v)[8][4], float m0, float l0, float m1, float l1) {
+        float4* dst = p.ws_o + ((int64_t)slot * kNT + t) * 256 + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) __stcg(dst + 32 * i, make_float4(v[i][0], v[i][1], v[i][2], v[i][3]));
+        if (r == 0) __stcg(p.ws_ml + ((int64_t)slot * kNT + t) * 4 + c, make_float4(m0, l0, m1, l1));
+    };
+
+    // Finishes the piece of the current segment whose last page is j_last.
+    auto finish_piece = [&](int j_last) {
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], off);
+        if (piece_j0 == 0 && j_last == nb - 1) {                // the whole segment
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) write_out(t, o[t], 1.f / l[t][0], 1.f / l[t][1]);
+            return;
+        }
+        const int seg_first = prefix[b] + seg * nb;
+        const int k_first = worker_of(seg_first, U, W);
+        const int k_last = worker_of(seg_first + nb - 1, U, W);
+        auto slot_of_piece = [&](int q) {
+            const int k = k_first + q;
+            return 2 * k + (range_start(k, U, W) >= seg_first ? 0 : 1);
+        };
+        int item = worker - k_first, n_items = k_last - k_first + 1, span = 1;
+        {
+            const int slot = slot_of_piece(item);
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) store_item(slot, t, o[t], m[t][0], l[t][0], m[t][1], l[t][1]);
+        }
+        for (int lvl = 0;; ++lvl) {
+            const int first = item - item % kMergeFan, last = min(first + kMergeFan, n_items) - 1;
+            const int cslot = slot_of_piece(first * span);
+            unsigned int* cnt = p.ws_count + (int64_t)lvl * 2 * W_total + cslot;
+            // the warp barrier orders every lane's stores before lane 0's release-acquire ticket;
+            // the merger's loads follow its acquire
+            __syncwarp();
+            unsigned int prev = 0;
+            if (lane == 0) prev = atomic_add_acq_rel_gpu(cnt, 1u);
+            prev = __shfl_sync(0xffffffffu, prev, 0);
+            if (prev != (unsigned int)(last - first)) return;   // another item merges the group
+            const int n_it = last - first + 1;
+            const int my_slot = lane < n_it ? slot_of_piece((first + lane) * span) : 0;
+            const int n_next = (n_items + kMergeFan - 1) / kMergeFan;
+#pragma unroll 1
+            for (int t = 0; t < kNT; ++t) {
+                auto load_vals = [&](float4 (&dst)[2][8], int k) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (k + u < n_it) {
+                            const int slot = __shfl_sync(0xffffffffu, my_slot, k + u);
+                            const float4* src = p.ws_o + ((int64_t)slot * kNT + t) * 256 + lane;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dst[u][i] = __ldcg(src + 32 * i);
+                        }
+                };
+                float4 va[2][8];
+                load_vals(va, 0);
+                float mm[8], ll[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float4 a = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                    if (lane < n_it) a = __ldcg(p.ws_ml + ((int64_t)my_slot * kNT + t) * 4 + k);
+                    mm[2 * k] = a.x; ll[2 * k] = a.y; mm[2 * k + 1] = a.z; ll[2 * k + 1] = a.w;
+                }
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    float M = mm[h];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+                    const float w = fast_exp2(mm[h] - fmaxf(M, kLogitFloor));   // 0 for an item that saw nothing
+                    float L = w * ll[h];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+                    wts[lane * 8 + h] = w;
+                    if (lane == 0) {
+                        wts[256 + h] = M;
+                        wts[264 + h] = L;
+                    }
+                }
+                __syncwarp();
+                float acc[8][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < n_it; k += 2) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (k + u < n_it) {
+                            const float w0 = wts[(k + u) * 8 + 2 * c], w1 = wts[(k + u) * 8 + 2 * c + 1];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                acc[i][0] += w0 * va[u][i].x; acc[i][1] += w1 * va[u][i].y;
+                                acc[i][2] += w0 * va[u][i].z; acc[i][3] += w1 * va[u][i].w;
+                            }
+                        }
+                    if (k + 2 < n_it) load_vals(va, k + 2);
+                }
+                const float M0 = wts[256 + 2 * c], M1 = wts[256 + 2 * c + 1];
+                const float L0 = wts[264 + 2 * c], L1 = wts[264 + 2 * c + 1];
+                __syncwarp();
+                if (n_next == 1) write_out(t, acc, 1.f / L0, 1.f / L1);
+                else store_item(cslot, t, acc, M0, L0, M1, L1);   // the group is one item of the next level
+            }
+            if (lane == 0) *cnt = 0u;                             // ready for the next call
+            if (n_next == 1) return;
+            item = first / kMergeFan;
+            n_items = n_next;
+            span *= kMergeFan;
+        }
+    };
+
+    // A wait that ran out (flagged) ends this worker, after the copies it issued have landed.
+    auto drain_after = [&](int lost) {
+        for (int u = lost + 1; u < issued; ++u) mbar_wait(full_bar(u % kStages), (u / kStages) & 1);
+    };
+    constexpr bool kPairs = kNT == 1 && kStages >= 2;            // two pages a step for a single column tile
+    for (int t = 0; t < n; ++t) {
+        const int s = t % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(full_bar(s), (t / kStages) & 1))) {
+            drain_after(t);
+            return;
+        }
+        bool pair = false;
+        if constexpr (kPairs) {
+            pair = j + 1 < nb && t + 1 < n;
+            if (pair) {
+                const int s2 = (t + 1) % kStages;
+                if (!__all_sync(0xffffffffu, mbar_wait(full_bar(s2), ((t + 1) / kStages) & 1))) {
+                    drain_after(t + 1);
+                    return;
+                }
+                attend(std::integral_constant<int, 2>(), s, s2, j);
+                __syncwarp();
+                if (t + kStages < n) issue(t + kStages);
+                if (t + 1 + kStages < n) issue(t + 1 + kStages);
+                ++t;                                              // the cursor moves to the second page
+                ++j;
+            }
+        }
+        if (!pair) {
+            attend(std::integral_constant<int, 1>(), s, s, j);
+            __syncwarp();
+            if (t + kStages < n) issue(t + kStages);
+        }
+        const bool seg_end = j == nb - 1;
+        if (seg_end || t == n - 1) {
+            finish_piece(j);
+            if (t == n - 1) break;
+            // (a range's last unit always closes a piece, so here the segment ended)
+            j = 0;
+            if (++seg == (prefix[b + 1] - prefix[b]) / nb) {
+                seg = 0;
+                do { ++b; } while (prefix[b + 1] == prefix[b]);
+                nb = pages_of(b);
+            }
+            __syncwarp();
+            open_segment();
+            reset();
+            piece_j0 = 0;
+        } else {
+            ++j;
+        }
+    }
+}
+
+}  // namespace pkv
