@@ -644,9 +644,10 @@ pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void*
  * query tokens per sequence, the last ones of its context, causal) over an
  * 8-bit cache: from a few drafted tokens per sequence to long prefill chunks.
  * `workspace` (paged_gqa_prefill_workspace_size(..., PKV_KV_INT8) bytes) is
- * required, with the rules of paged_gqa_decode_attention_int8; so are its
- * limits on the batch, counted with the query groups a long chunk is cut into.
- * Sequences with inconsistent lengths are flagged and their rows left alone.
+ * required, with the rules of paged_gqa_decode_attention_int8. Chunks of more
+ * than 8 (query token, head of a KV head) pairs run on the tensor cores with
+ * cached values rounded to f16 (magnitudes past its range saturate). Sequences
+ * with inconsistent lengths are flagged and their rows left alone.
  */
 pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
                                             const float* kv_scales,

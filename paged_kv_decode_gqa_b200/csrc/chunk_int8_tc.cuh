@@ -1,0 +1,847 @@
+// Attention of a chunk of new tokens over the 8-bit paged cache, on the
+// fifth-generation tensor cores (tcgen05, TMEM accumulators).
+//
+// What it computes: query i of sequence b sits at position L_b - n_b + i and
+// attends causally to positions [0, p] of the sequence's 8-bit cache
+// (int8_cache.cuh), query head h reading KV head h / G. A cached value is
+// (code - 128) * scale, rounded to f16 as it is staged for the tensor cores
+// (half a step, 2^-11; values past the f16 range saturate).
+//
+// Structure (one CTA per SM, persistent):
+//  * A query tile is T = floor(128 / G) query tokens x the G heads of one KV
+//    head, row r = (token r / G, head r % G). A KV tile is 128 tokens. S = Q K^T
+//    and O += P V are M = N = K = 128 products, P over S in TMEM; two softmax
+//    streams (S, O and four warps each) keep the tensor cores on one stream's
+//    products while the other's softmax runs.
+//  * Wide (chunks longer than T): the streams are two query tiles that share
+//    every KV tile. Narrow (chunks that fit one query tile, such as drafted
+//    tokens): the streams are the even and the odd KV tiles of one query tile,
+//    so that the cache is read at twice the rate of one stream's chain of
+//    products and softmax; the two partial results of a row meet in TMEM (softmax
+//    warps w and w + 4 share its lanes).
+//  * Load balance: the items (query group, KV head, sequence) form a row of
+//    KV tiles, every CTA takes an equal run of it, an item cut between CTAs is
+//    computed in pieces that store (max, sum, O) per row, and the piece that
+//    takes the last ticket merges them. Nobody waits on another CTA.
+//  * Staging: two TMA warps bring pages of codes (128-byte swizzle) and their
+//    scales; four warps convert them, one token (row) per thread, so that the
+//    token's scale is a register: a code becomes an exact f16 integer (a byte
+//    permute and a subtraction), and code * scale is formed in f16x2 as
+//    code * hi + (code * lo) with scale = hi + lo split into two f16, which
+//    leaves one rounding (rows whose scale is below 2^-12, where lo would be
+//    subnormal, go through fp32). The f16 tiles are written in the 128-byte
+//    swizzled layout the tensor cores read: K and V are double-buffered.
+//    Codes are finite and rows past the context get scale 0, so no row needs
+//    clearing.
+//  * Softmax: a row per thread. The running maximum (exp2 domain) is raised
+//    only by more than 8, so most tiles rescale nothing; the row sum adds the
+//    probabilities as rounded to f16. Warps with no live row do no work.
+// Every wait is bounded; one that runs out flags PKV_DEVERR_WAIT_TIMEOUT and
+// every role stops, drains what it has in flight and leaves; TMEM is freed.
+#pragma once
+
+#include "int8_cache.cuh"
+#include "prefill_tc.cuh"
+#include "stream_int8.cuh"
+
+namespace pkv {
+
+struct ChunkInt8Params {
+    __half* out;                  // [total, Hq, 128]
+    const int32_t* block_tables;  // [B, max_blocks_per_seq]
+    const int32_t* context_lens;  // [B]
+    const int32_t* query_start;   // [B + 1]
+    uint8_t* parts;               // [2 * CTAs][2 streams][kPartBytes]
+    unsigned int* tickets;        // [CTAs][2][4], zero between calls
+    int32_t batch, total, max_query_len;
+    int32_t Hq, Hkv, G;
+    int32_t max_blocks_per_seq, num_blocks, max_context_len;
+    int32_t tokens;               // T: query tokens of a tile
+    float logit_scale_log2;       // |softmax_scale| * log2(e)
+    float key_sign;               // sign of softmax_scale, applied to the keys
+};
+
+struct ChunkInt8Shape {
+    static constexpr int kKvTok = 128;
+    static constexpr int kChunk = 128 * 128;            // 64 channels of 128 rows, f16: 16 KiB
+    static constexpr int kTile = 2 * kChunk;            // a 128 x 128 f16 tile
+    static constexpr int kRaw = 128 * 128;              // codes of K or V of a KV tile
+    static constexpr int kScales = 8 * 128;             // scales of a KV tile: 8 pages x (16 K, 16 V)
+    static constexpr int kBarBytes = 256;
+    // Q A | Q B or a second raw stage | K x 2 | V x 2 | raw K, V | scales x 2 | barriers and words.
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = 2 * kTile;
+    static constexpr int kOffV = kOffK + 2 * kTile;
+    static constexpr int kOffRaw = kOffV + 2 * kTile;
+    static constexpr int kOffScales = kOffRaw + 2 * kRaw;
+    static constexpr int kOffBars = kOffScales + 2 * kScales;
+    static constexpr int kOffWords = kOffBars + kBarBytes;   // block scan [16], first sequence [2], abort flag
+    static constexpr int kSmemBytes = kOffWords + 256;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory of one SM");
+    static constexpr int kSoftmaxWarps = 8;
+    static constexpr int kConvertWarp = 8;              // 8..11
+    static constexpr int kTmaKWarp = 12, kTmaVWarp = 13, kMmaWarp = 14;
+    static constexpr int kThreads = 32 * 15;
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr float kRescaleThreshold = 8.f;
+    static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
+};
+
+// Four codes to four f16 of code * (hi + lo), rounded once (to within 2^-22).
+__device__ __forceinline__ void dequant4(uint32_t w, __half2 hi, __half2 lo, uint32_t& d0, uint32_t& d1) {
+    uint32_t a, b;
+    codes_to_half2x2(w, a, b);
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&b);
+    const __half2 u = __hfma2(x, hi, __hmul2(x, lo)), v = __hfma2(y, hi, __hmul2(y, lo));
+    d0 = *reinterpret_cast<const uint32_t*>(&u);
+    d1 = *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void dequant4_small(uint32_t w, float s, uint32_t& d0, uint32_t& d1) {
+    auto f = [&](int k) { return (float)((int)((w >> (8 * k)) & 0xff) - 128) * s; };
+    d0 = pack_half2(f(0), f(1));
+    d1 = pack_half2(f(2), f(3));
+}
+
+template <bool kNarrow>
+__global__ void __launch_bounds__(ChunkInt8Shape::kThreads, 1)
+chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_s,
+                  const ChunkInt8Params p) {
+    using S = ChunkInt8Shape;
+    constexpr int kRawStages = kNarrow ? 2 : 1;
+    constexpr int kQTiles = kNarrow ? 1 : 2;             // query tiles of an item
+    constexpr int kMinTiles = kNarrow ? 2 : 4;           // fewest KV tiles a CTA is given
+    extern __shared__ uint8_t smem_raw[];
+    // Without a static part the dynamic shared memory starts at a multiple of 1024 bytes, and its 226.5 KiB
+    // leave no room to align it here. (An alignment on the declaration would pad every kernel of the library.)
+    const uint32_t base = smem_u32(smem_raw);
+    if (base & 1023u) {
+        flag_error(PKV_DEVERR_WAIT_TIMEOUT);             // never seen: no operand tile could be addressed
+        return;
+    }
+    long long* s_red = reinterpret_cast<long long*>(smem_raw + S::kOffWords);     // [16]
+    long long* s_first = s_red + 16;                                              // [2]
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_first + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.G, T = p.tokens;
+    const int per_item = kQTiles * T;                    // query tokens of an item
+
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int cap = min(p.max_context_len, p.max_blocks_per_seq * kPageRows);
+    // lengths of sequence b; false (no queries) when they are inconsistent
+    auto lengths = [&](int b, int& qs0, int& n, int& L) -> bool {
+        qs0 = __ldg(p.query_start + b);
+        const int qs1 = __ldg(p.query_start + b + 1);
+        L = __ldg(p.context_lens + b);
+        n = qs1 - qs0;
+        return !(qs0 < 0 || qs1 < qs0 || qs1 > p.total || n > p.max_query_len || L < n || L > cap);
+    };
+    // KV tiles of all items of sequence b under one KV head
+    auto seq_tiles = [&](int b) -> int64_t {
+        int qs0, n, L;
+        if (!lengths(b, qs0, n, L)) return 0;
+        int64_t s = 0;
+        for (int i0 = 0; i0 < n; i0 += per_item) s += (L - n + min(i0 + per_item, n) - 1) / S::kKvTok + 1;
+        return s;
+    };
+    // inclusive scan of x over the block; total: the block's sum (ends synchronised)
+    auto block_scan = [&](int64_t x, int64_t& total) -> int64_t {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) s_red[warp] = x;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+        for (int i = 0; i < S::kThreads / 32; ++i) {
+            before += i < warp ? s_red[i] : 0;
+            total += s_red[i];
+        }
+        __syncthreads();
+        return before + x;
+    };
+    // ---- the batch's KV tiles ("units") and this CTA's run of them ----
+    int64_t U = 0, u_lo, u_hi;
+    int ctas;
+    {
+        int64_t my_w = 0, my_incl = 0, first_total = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += S::kThreads) {
+            const int b = b0 + (int)threadIdx.x;
+            int64_t w = 0;
+            if (b < p.batch) {
+                w = seq_tiles(b) * p.Hkv;
+                int qs0, n, L;
+                if (blockIdx.x == 0 && !lengths(b, qs0, n, L)) flag_error(PKV_DEVERR_CONTEXT_LEN);
+            }
+            int64_t total;
+            const int64_t incl = U + block_scan(w, total);
+            if (b0 == 0) {
+                my_w = w;
+                my_incl = incl;
+                first_total = total;
+            }
+            U += total;
+        }
+        ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, U / kMinTiles));
+        u_lo = blockIdx.x < ctas ? (int64_t)blockIdx.x * U / ctas : U;
+        u_hi = blockIdx.x < ctas ? ((int64_t)blockIdx.x + 1) * U / ctas : U;
+        if (u_lo < u_hi) {
+            if (my_w > 0 && my_incl - my_w <= u_lo && u_lo < my_incl) {
+                s_first[0] = threadIdx.x;
+                s_first[1] = my_incl - my_w;
+            }
+            int64_t base = first_total;                  // more sequences than threads: scan again
+            for (int b0 = S::kThreads; b0 < p.batch && base <= u_lo; b0 += S::kThreads) {
+                const int b = b0 + (int)threadIdx.x;
+                const int64_t w = b < p.batch ? seq_tiles(b) * p.Hkv : 0;
+                int64_t total;
+                const int64_t incl = base + block_scan(w, total);
+                if (w > 0 && incl - w <= u_lo && u_lo < incl) {
+                    s_first[0] = b;
+                    s_first[1] = incl - w;
+                }
+                base += total;
+            }
+        }
+        __syncthreads();
+    }
+    if (u_lo >= u_hi) return;                            // no work for this CTA (uniform)
+    auto range_lo = [&](int c) -> int64_t { return (int64_t)c * U / ctas; };
+    auto cta_of = [&](int64_t u) -> int {
+        int c = (int)min((int64_t)ctas - 1, u * ctas / U);
+        while (c > 0 && range_lo(c) > u) --c;
+        while (c + 1 < ctas && range_lo(c + 1) <= u) ++c;
+        return c;
+    };
+    // The CTA's pieces, in order: KV tiles [j0, j1) of an item.
+    struct Cursor { int b, g, q; int64_t u; };
+    struct Piece { int b, g, row0, nq, pos0, ntiles, npages, L, j0, j1; int64_t u; };
+    Cursor start;
+    {
+        start.b = (int)s_first[0];
+        const int64_t per_g = seq_tiles(start.b);
+        start.g = (int)((u_lo - s_first[1]) / per_g);
+        start.u = s_first[1] + start.g * per_g;
+        start.q = 0;
+        int qs0, n, L;
+        lengths(start.b, qs0, n, L);
+        for (int i0 = 0; i0 < n; i0 += per_item) {
+            const int ntiles = (L - n + min(i0 + per_item, n) - 1) / S::kKvTok + 1;
+            if (start.u + ntiles > u_lo) break;
+            start.u += ntiles;
+            ++start.q;
+        }
+    }
+    auto next_piece = [&](Cursor& cu, Piece& pc) -> bool {
+        while (cu.u < u_hi && cu.b < p.batch) {
+            int qs0, n, L;
+            const bool ok = lengths(cu.b, qs0, n, L);
+            const int i0 = cu.q * per_item;
+            if (!ok || i0 >= n) {                        // next KV head, or next sequence
+                cu.q = 0;
+                if (!ok || n == 0 || ++cu.g == p.Hkv) {
+                    cu.g = 0;
+                    ++cu.b;
+                }
+                continue;
+            }
+            pc.b = cu.b;
+            pc.g = cu.g;
+            pc.row0 = qs0 + i0;
+            pc.nq = min(per_item, n - i0);
+            pc.pos0 = L - n + i0;
+            const int p_max = pc.pos0 + pc.nq - 1;
+            pc.ntiles = p_max / S::kKvTok + 1;
+            pc.npages = p_max / kPageRows + 1;
+            pc.L = L;
+            pc.u = cu.u;
+            pc.j0 = (int)(max(cu.u, u_lo) - cu.u);
+            pc.j1 = (int)(min(cu.u + pc.ntiles, u_hi) - cu.u);
+            cu.u += pc.ntiles;
+            ++cu.q;
+            return true;
+        }
+        return false;
+    };
+
+    // ---- shared memory, barriers, TMEM ----
+    auto q_s = [&](int t) { return base + S::kOffQ + t * S::kTile; };
+    auto k_s = [&](int s) { return base + S::kOffK + s * S::kTile; };
+    auto v_s = [&](int s) { return base + S::kOffV + s * S::kTile; };
+    // raw stage 0 has its own place, stage 1 (narrow) that of the second query tile
+    auto raw_k = [&](int s) { return base + (s ? S::kOffQ + S::kTile : S::kOffRaw); };
+    auto raw_v = [&](int s) { return raw_k(s) + S::kRaw; };
+    auto raw_sc = [&](int s) { return base + S::kOffScales + s * S::kScales; };
+    const uint32_t bars = base + S::kOffBars;
+    const uint32_t q_full = bars, q_empty = bars + 8, drain = bars + 16;
+    auto s_full = [&](int t) { return bars + 24 + 8u * t; };
+    auto p_full = [&](int t) { return bars + 40 + 8u * t; };
+    auto o_done = [&](int t) { return bars + 56 + 8u * t; };
+    auto o_free = [&](int t) { return bars + 72 + 8u * t; };
+    auto k_full = [&](int s) { return bars + 88 + 8u * s; };
+    auto k_empty = [&](int s) { return bars + 104 + 8u * s; };
+    auto v_full = [&](int s) { return bars + 120 + 8u * s; };
+    auto v_empty = [&](int s) { return bars + 136 + 8u * s; };
+    auto rk_full = [&](int s) { return bars + 152 + 8u * s; };
+    auto rk_empty = [&](int s) { return bars + 168 + 8u * s; };
+    auto rv_full = [&](int s) { return bars + 184 + 8u * s; };
+    auto rv_empty = [&](int s) { return bars + 200 + 8u * s; };
+    // narrow: the odd stream's (m, l) of a piece are in TMEM; the even stream has read them
+    const uint32_t x_full = bars + 216, x_read = bars + 224;
+    const uint32_t tmem_slot = bars + 240;
+    const int rows = G * T;                              // rows of Q the TMA fills; the rest stay zero
+    if (threadIdx.x == 0) {
+        *s_abort = 0;
+        mbar_init(x_full, 128);
+        mbar_init(x_read, 128);
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(drain, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), 128);
+            mbar_init(o_done(t), 1);
+            mbar_init(o_free(t), 128);
+            mbar_init(k_full(t), 4);
+            mbar_init(k_empty(t), 1);
+            mbar_init(v_full(t), 4);
+            mbar_init(v_empty(t), 1);
+            mbar_init(rk_full(t), 1);
+            mbar_init(rk_empty(t), 4);
+            mbar_init(rv_full(t), 1);
+            mbar_init(rv_empty(t), 4);
+        }
+        mbar_init_fence();
+    }
+    for (int i = threadIdx.x; i < kQTiles * (128 - rows) * 16; i += S::kThreads) {
+        const int t = i / ((128 - rows) * 16), k = i % ((128 - rows) * 16);
+        const int r = rows + k / 16, part = k % 16;
+        const uint32_t a = q_s(t) + (part >> 3) * S::kChunk + r * 128 + (part & 7) * 16;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(a), "r"(0u) : "memory");
+    }
+    fence_proxy_async_shared();
+    if (warp == S::kMmaWarp) {
+        tmem_alloc(tmem_slot, S::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    auto tmem_s = [&](int t) { return tmem + 128u * t; };
+    auto tmem_o = [&](int t) { return tmem + 256u + 128u * t; };
+
+    // Bounded wait that also gives up once another role has given up.
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t it = 0;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 63u) == 63u) {
+                if (*s_abort) return false;
+                if (global_timer_ns() - t0 > kWaitLimitNs) {
+                    flag_error(PKV_DEVERR_WAIT_TIMEOUT);
+                    *s_abort = 1;
+                    return false;
+                }
+            }
+        }
+    };
+    auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+    if (warp == S::kTmaKWarp || warp == S::kTmaVWarp) {
+        // ================= TMA: codes of K (with Q and the scales), or of V =================
+        const bool is_k = warp == S::kTmaKWarp;
+        const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+        if (lane == 0) {
+            prefetch_tensormap(map);
+            if (is_k) {
+                prefetch_tensormap(&tm_q);
+                prefetch_tensormap(&tm_s);
+            }
+        }
+        auto full = [&](int s) { return is_k ? rk_full(s) : rv_full(s); };
+        auto empty = [&](int s) { return is_k ? rk_empty(s) : rv_empty(s); };
+        int gj = 0, k = 0;
+        bool ok = true;
+        Cursor cu = start;
+        Piece pc;
+        while (ok && next_piece(cu, pc)) {
+            const int32_t* bt = p.block_tables + (int64_t)pc.b * p.max_blocks_per_seq;
+            for (int j = pc.j0; j < pc.j1; ++j, ++gj) {
+                const int s = gj % kRawStages;
+                // a page per lane; pages past the item's last position are not loaded (their scales are
+                // taken as 0 by position)
+                const int pages = min(8, pc.npages - 8 * j);
+                int pb = -1;
+                if (lane < pages) {
+                    pb = __ldg(bt + 8 * j + lane);
+                    if (pb < 0 || pb >= p.num_blocks) {  // outside the pool: codes and scales read as zeros
+                        if (is_k) flag_error(PKV_DEVERR_BLOCK_ID);
+                        pb = -1;
+                    }
+                }
+                if (gj >= kRawStages && !(ok = wait_all(empty(s), ((gj / kRawStages) - 1) & 1))) break;
+                if (lane == 0) mbar_arrive_expect_tx(full(s), pages * (2048 + (is_k ? 128 : 0)));
+                __syncwarp();
+                if (lane < pages) {
+                    fence_proxy_async_shared();          // the converters' reads of the stage come first
+                    const uint32_t dst = (is_k ? raw_k(s) : raw_v(s)) + lane * 2048;
+                    tma_load_3d_reused(dst, map, full(s), 0, pc.g, pb * kPageRows);
+                    if (is_k) tma_load_3d_reused(raw_sc(s) + lane * 128, &tm_s, full(s), 0, pc.g, pb);
+                }
+                __syncwarp();
+                if (is_k && j == pc.j0) {                // the piece's Q, behind its first K
+                    if (k >= 1 && !(ok = wait_all(q_empty, (k - 1) & 1))) {
+                        ++gj;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, kQTiles * 2 * 128 * rows);
+                        for (int t = 0; t < kQTiles; ++t) {
+                            tma_load_3d_reused(q_s(t), &tm_q, q_full, 0, pc.g * G, pc.row0 + t * T);
+                            tma_load_3d_reused(q_s(t) + S::kChunk, &tm_q, q_full, 64, pc.g * G, pc.row0 + t * T);
+                        }
+                    }
+                    __syncwarp();
+                    ++k;
+                }
+            }
+        }
+        // nothing of ours may be in flight when the CTA leaves
+        for (int j = max(0, gj - kRawStages); j < gj; ++j) mbar_wait(full(j % kRawStages), (j / kRawStages) & 1);
+        if (is_k && k >= 1) mbar_wait(q_full, (k - 1) & 1);
+    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + 4) {
+        // ========================= codes to f16 tiles: a token per thread =========================
+        const int row = 32 * (warp - S::kConvertWarp) + lane;      // token of the KV tile
+        const uint32_t sw = (uint32_t)(row & 7);
+        // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`
+        auto convert = [&](uint32_t src, uint32_t dst, float s) {
+            const float a = fabsf(s);
+            const bool small = a < 2.44140625e-4f;                 // 2^-12; 0 included
+            const __half hi = __float2half_rn(s);
+            const __half lo = __float2half_rn(s - __half2float(hi));
+            const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+            const uint32_t in = src + row * 128, out = dst + row * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {                          // 16 channels a step
+                const uint4 w = lds128(in + ((c ^ sw) << 4));
+                uint32_t d[8];
+                if (!small) {
+                    dequant4(w.x, hi2, lo2, d[0], d[1]);
+                    dequant4(w.y, hi2, lo2, d[2], d[3]);
+                    dequant4(w.z, hi2, lo2, d[4], d[5]);
+                    dequant4(w.w, hi2, lo2, d[6], d[7]);
+                } else {
+                    dequant4_small(w.x, s, d[0], d[1]);
+                    dequant4_small(w.y, s, d[2], d[3]);
+                    dequant4_small(w.z, s, d[4], d[5]);
+                    dequant4_small(w.w, s, d[6], d[7]);
+                }
+                const uint32_t o = out + (c >> 2) * S::kChunk;
+                const uint32_t c0 = (uint32_t)(2 * (c & 3));
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(o + ((c0 ^ sw) << 4)), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(o + (((c0 + 1) ^ sw) << 4)), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]) : "memory");
+            }
+        };
+        // the row's scale: 0 past the context; outside [0, 2^60] flagged and 0; saturating at the f16 range
+        auto row_scale = [&](const Piece& pc, int j, uint32_t addr) -> float {
+            const float s = lds32(addr);
+            const bool live = j * S::kKvTok + row < min(pc.L, pc.npages * kPageRows);
+            const bool fine = s >= 0.f && s <= kScaleMax;
+            if (live && !fine) flag_error(PKV_DEVERR_SCALE);
+            return live && fine ? fminf(s, 511.75f) : 0.f;
+        };
+        const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4);
+        Cursor cu = start;
+        Piece pc;
+        int gj = 0;                                                // KV tiles of earlier pieces
+        float v_scale[2] = {0.f, 0.f};                             // of the tiles whose K is converted, V not yet
+        auto do_k = [&](int i) -> bool {
+            const int g = gj + i, s = g % kRawStages, d = g & 1;
+            if (!wait_all(rk_full(s), (g / kRawStages) & 1)) return false;
+            const float ks = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
+            const float vs = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
+            if (d) v_scale[1] = vs;
+            else v_scale[0] = vs;
+            if (g >= 2 && !wait_all(k_empty(d), ((g >> 1) - 1) & 1)) return false;
+            convert(raw_k(s), k_s(d), ks);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(rk_empty(s));
+                mbar_arrive(k_full(d));
+            }
+            return true;
+        };
+        auto do_v = [&](int i) -> bool {
+            const int g = gj + i, s = g % kRawStages, d = g & 1;
+            if (!wait_all(rv_full(s), (g / kRawStages) & 1)) return false;
+            if (g >= 2 && !wait_all(v_empty(d), ((g >> 1) - 1) & 1)) return false;
+            convert(raw_v(s), v_s(d), d ? v_scale[1] : v_scale[0]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(rv_empty(s));
+                mbar_arrive(v_full(d));
+            }
+            return true;
+        };
+        bool ok = true;
+        while (ok && next_piece(cu, pc)) {                         // K runs one tile ahead of V
+            const int n = pc.j1 - pc.j0;
+            ok = do_k(0);
+            for (int i = 0; ok && i < n; ++i) {
+                if (i + 1 < n) ok = do_k(i + 1);
+                if (ok) ok = do_v(i);
+            }
+            gj += n;
+        }
+    } else if (warp == S::kMmaWarp) {
+        // ===================================== MMA =====================================
+        constexpr uint32_t kIdescS = umma_idesc_f16(128, 128, 0);    // Q K^T: both K-major
+        constexpr uint32_t kIdescPV = umma_idesc_f16(128, 128, 1);   // P V: V is MN-major
+        // S_t = Q K(gg)^T, once stream t's previous O_t += P_t V (its cnt-th) has read P_t out of S_t
+        auto issue_s = [&](int t, int gg, int cnt, bool free_k, bool last) -> bool {
+            if (cnt >= 1 && !wait_all(o_done(t), (cnt - 1) & 1)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const int s = gg & 1;
+                const uint32_t q = q_s(kNarrow ? 0 : t);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t koff = (kk >> 2) * S::kChunk + (kk & 3) * 32;
+                    umma_f16_ss(tmem_s(t), umma_desc_sw128(q + koff, 16, 1024), umma_desc_sw128(k_s(s) + koff, 16, 1024),
+                                kIdescS, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(s_full(t));
+                if (free_k) umma_commit(k_empty(s));
+                if (last) umma_commit(q_empty);
+            }
+            __syncwarp();
+            return true;
+        };
+        // O_t += P_t V(gg); `first`: the piece's first product on the stream overwrites O_t
+        auto issue_pv = [&](int t, int gg, int cnt, bool free_v, bool first) -> bool {
+            if (!wait_all(p_full(t), cnt & 1)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const int s = gg & 1;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_f16_ts(tmem_o(t), tmem_s(t) + 8 * kk, umma_desc_sw128(v_s(s) + kk * 2048, S::kChunk, 1024),
+                                kIdescPV, (!first || kk > 0) ? 1u : 0u);
+                umma_commit(o_done(t));
+                if (free_v) umma_commit(v_empty(s));
+            }
+            __syncwarp();
+            return true;
+        };
+        int gj = 0, k = 0;
+        int cnt[2] = {0, 0}, used[2] = {0, 0};           // products and pieces of each stream so far
+        bool ok = true;
+        Cursor cu = start;
+        Piece pc;
+        while (ok && next_piece(cu, pc)) {
+            int n = pc.j1 - pc.j0;
+            asm volatile("" : "+r"(n));                  // kept in a register for the issue loop
+            if (!(ok = wait_all(q_full, k & 1))) break;
+            if constexpr (kNarrow) {
+                // KV tile i on stream i & 1: S(0), S(1), then P V(i), S(i + 2)
+                auto s_of = [&](int i) -> bool {
+                    return wait_all(k_full((gj + i) & 1), ((gj + i) >> 1) & 1) &&
+                           issue_s(i & 1, gj + i, (i & 1 ? cnt[1] : cnt[0]) + (i >> 1), true, i == n - 1);
+                };
+                ok = s_of(0);
+                // the first S on the odd stream overwrites the (m, l) of its previous piece
+                if (ok && n > 1 && used[1] >= 1) ok = wait_all(x_read, (used[1] - 1) & 1);
+                if (ok && n > 1) ok = s_of(1);
+                for (int i = 0; ok && i < n; ++i) {
+                    const int t = i & 1;
+                    if (!(ok = wait_all(v_full((gj + i) & 1), ((gj + i) >> 1) & 1))) break;
+                    const int u = t ? used[1] : used[0];
+                    if (i < 2 && u >= 1 && !(ok = wait_all(o_free(t), (u - 1) & 1))) break;
+                    ok = issue_pv(t, gj + i, (t ? cnt[1] : cnt[0]) + (i >> 1), true, i < 2);
+                    if (ok && i + 2 < n) ok = s_of(i + 2);
+                }
+                cnt[0] += (n + 1) >> 1;
+                cnt[1] += n >> 1;
+                ++used[0];
+                used[1] += n > 1 ? 1 : 0;
+            } else {
+                if (!(ok = wait_all(k_full(gj & 1), (gj >> 1) & 1))) break;
+                for (int t = 0; ok && t < 2; ++t) ok = issue_s(t, gj, gj, t == 1, t == 1 && n == 1);
+                // per KV tile: O_A += P_A V, S_A of the next, O_B += P_B V, S_B of the next
+                for (int i = 0; ok && i < n; ++i) {
+                    const int gg = gj + i;
+                    if (!(ok = wait_all(v_full(gg & 1), (gg >> 1) & 1))) break;
+                    const bool more = i + 1 < n;
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if (i == 0 && k >= 1 && !(ok = wait_all(o_free(t), (k - 1) & 1))) break;
+                        ok = issue_pv(t, gg, gg, t == 1, i == 0);
+                        if (ok && more && t == 0) ok = wait_all(k_full((gg + 1) & 1), ((gg + 1) >> 1) & 1);
+                        if (ok && more) ok = issue_s(t, gg + 1, gg + 1, t == 1, t == 1 && i + 2 == n);
+                    }
+                }
+            }
+            gj += n;
+            ++k;
+        }
+        if (lane == 0) umma_commit(drain);               // every product has completed before TMEM is freed
+        __syncwarp();
+        mbar_wait(drain, 0);
+    } else {
+        // =================================== softmax ===================================
+        const int quarter = warp & 3, t = warp >> 2;             // rows, and the stream served
+        const int r = 32 * quarter + lane;                       // row = TMEM lane
+        const int ti = r / G, hh = r - ti * G;
+        const int qi = (kNarrow ? 0 : t * T) + ti;               // query within the item
+        const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+        const uint32_t s_row = tmem_s(t) + lane_base, o_row = tmem_o(t) + lane_base;
+        const float sl = p.logit_scale_log2;
+        int cnt = 0, exchanges = 0;                              // the stream's KV tiles; rows handed over
+        bool ok = true;
+        Cursor cu = start;
+        Piece pc;
+        while (ok && next_piece(cu, pc)) {
+            const int n = pc.j1 - pc.j0;
+            const int mine = kNarrow ? (n + 1 - t) >> 1 : n;     // KV tiles of this stream
+            if (mine == 0) continue;                             // a one-tile piece has no odd stream
+            const bool valid = r < rows && qi < pc.nq;
+            const bool idle = !__any_sync(0xffffffffu, valid);
+            const int prow = pc.pos0 + min(qi, pc.nq - 1);       // causal limit of the row
+            const int first_pos = pc.pos0 + (kNarrow ? 0 : t * T);
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int i = 0; i < mine; ++i, ++cnt) {
+                if (!(ok = wait_all(s_full(t), cnt & 1))) break;
+                if (idle) {                                      // no live row in this warp: P is not used
+                    mbar_arrive(p_full(t));
+                    continue;
+                }
+                tc_fence_after();
+                const int t0 = (pc.j0 + (kNarrow ? 2 * i + t : i)) * S::kKvTok;
+                const bool edge = t0 + S::kKvTok - 1 > first_pos;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float x[2][32];
+                    tmem_ld32x2(s_row + 64 * h, x[0], s_row + 64 * h + 32, x[1]);
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2) {
+                        const int c = 2 * h + c2;
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                mx[e & 3] = fmaxf(mx[e & 3], t0 + 32 * c + e <= prow ? x[c2][e] : -INFINITY);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[c2][e]);
+                        }
+                    }
+                }
+                float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                mt = mt > -INFINITY ? mt * sl : -INFINITY;       // (a zero scale must not make -inf * 0)
+                const bool raise = mt > m_run + S::kRescaleThreshold;
+                const float m_new = raise ? mt : m_run;
+                // O_t is final for this tile: its last product completed before this S was issued
+                if (i > 0 && __any_sync(0xffffffffu, raise)) {
+                    const float alpha = raise ? fast_exp2(m_run - m_new) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        tmem_ld32(o_row + 32 * c, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(o_row + 32 * c, o);
+                    }
+                    l_run *= alpha;
+                }
+                m_run = m_new;
+                const float m_use = fmaxf(m_run, kLogitFloor);   // (a row that has seen nothing: all weights 0)
+                float lt[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float w[32];
+                    float xx[2][32];
+                    tmem_ld32x2(s_row + 64 * h, xx[0], s_row + 64 * h + 32, xx[1]);
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2) {
+                        const int c = 2 * h + c2;
+                        const float (&x)[32] = xx[c2];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float e0 = fmaf(x[2 * e], sl, -m_use), e1 = fmaf(x[2 * e + 1], sl, -m_use);
+                            if (edge) {
+                                e0 = t0 + 32 * c + 2 * e <= prow ? e0 : -INFINITY;
+                                e1 = t0 + 32 * c + 2 * e + 1 <= prow ? e1 : -INFINITY;
+                            }
+                            const uint32_t pw = pack_half2(fast_exp2(e0), fast_exp2(e1));
+                            lt[e & 3] = add_f16_hi(add_f16_lo(lt[e & 3], pw), pw);
+                            w[16 * c2 + e] = __uint_as_float(pw);
+                        }
+                    }
+                    tmem_st32(s_row + 32 * h, w);
+                }
+                l_run += (lt[0] + lt[1]) + (lt[2] + lt[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full(t));
+            }
+            if (!ok) break;
+            if (!(ok = wait_all(o_done(t), (cnt - 1) & 1))) break;
+            tc_fence_after();
+            // narrow: the odd stream hands its rows to the even one, whose warp reads both from TMEM
+            const bool both = kNarrow && n > 1;
+            float wa = 1.f, wb = 0.f;
+            if constexpr (kNarrow) {
+                const uint32_t ml_col = tmem_s(1) + lane_base + 126;   // past P in the odd stream's S
+                if (t == 1) {
+                    tmem_st1(ml_col, m_run);
+                    tmem_st1(ml_col + 1, l_run);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(x_full);
+                    continue;
+                }
+                if (both) {
+                    if (!(ok = wait_all(x_full, exchanges & 1))) break;
+                    ++exchanges;
+                    tc_fence_after();
+                    const float2 ml = make_float2(tmem_ld1(ml_col), tmem_ld1(ml_col + 1));
+                    tc_fence_before();
+                    mbar_arrive(x_read);
+                    const float M = fmaxf(fmaxf(m_run, ml.x), kLogitFloor);
+                    wa = fast_exp2(m_run - M);
+                    wb = fast_exp2(ml.x - M);
+                    l_run = l_run * wa + ml.y * wb;
+                    m_run = fmaxf(m_run, ml.x);
+                }
+            }
+            const uint32_t ob_row = tmem_o(1) + lane_base;
+            // columns 32 c .. 32 c + 31 of the row's unnormalised output
+            auto load_o = [&](int c, float (&o)[32]) {
+                if (both) {
+                    float ob[32];
+                    tmem_ld32x2(o_row + 32 * c, o, ob_row + 32 * c, ob);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = o[e] * wa + ob[e] * wb;
+                } else {
+                    tmem_ld32(o_row + 32 * c, o);
+                }
+            };
+            auto release_o = [&]() {                             // O may be overwritten
+                tc_fence_before();
+                mbar_arrive(o_free(t));
+                if (both) mbar_arrive(o_free(1));
+            };
+            if (idle) {
+                release_o();
+                continue;
+            }
+            __half* dst = p.out + ((int64_t)(pc.row0 + qi) * p.Hq + (int64_t)pc.g * G + hh) * kHeadDim;
+            auto store_out = [&](int c, const float (&o)[32], float inv) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint4 u;
+                    u.x = pack_half2(o[8 * q + 0] * inv, o[8 * q + 1] * inv);
+                    u.y = pack_half2(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
+                    u.z = pack_half2(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
+                    u.w = pack_half2(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+                    *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = u;
+                }
+            };
+            if (pc.j0 == 0 && pc.j1 == pc.ntiles) {
+                // ---- a whole item: out = O / l ----
+                const float inv = 1.f / l_run;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    load_o(c, o);
+                    if (valid) store_out(c, o, inv);
+                }
+                release_o();
+                continue;
+            }
+            // ---- a piece of an item cut at a CTA boundary: store (m, l, O), take a ticket for the
+            // warp's 32 rows; the last one merges out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k ----
+            const int c_first = cta_of(pc.u), c_last = cta_of(pc.u + pc.ntiles - 1);
+            auto part_of = [&](int c) -> uint8_t* {              // slot 0: the piece starts CTA c's run, else 1
+                const int slot = 2 * c + (max(pc.u, range_lo(c)) == range_lo(c) ? 0 : 1);
+                return p.parts + ((int64_t)slot * 2 + t) * S::kPartBytes;
+            };
+            {
+                uint8_t* part = part_of((int)blockIdx.x);
+                float4* po = reinterpret_cast<float4*>(part);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    load_o(c, o);
+                    if (valid) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            __stcg(po + (8 * c + q) * 128 + r, make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+                    }
+                }
+                if (valid) __stcg(reinterpret_cast<float2*>(part + 128 * 128 * 4) + r, make_float2(m_run, l_run));
+            }
+            release_o();
+            // the warp barrier orders every lane's stores before lane 0's release-acquire ticket; the
+            // merger's loads follow its acquire
+            __syncwarp();
+            unsigned int* tick = p.tickets + ((int64_t)c_last * 2 + t) * 4 + quarter;
+            unsigned int prev = 0;
+            if (lane == 0) prev = atomic_add_acq_rel_gpu(tick, 1u);
+            prev = __shfl_sync(0xffffffffu, prev, 0);
+            __syncwarp();
+            if (prev != (unsigned int)(c_last - c_first)) continue;   // another piece's warp merges
+            if (lane == 0) *tick = 0u;                           // ready for the next call
+            if (!valid) continue;
+            // in the order of the pieces, whoever merges: the result does not depend on timing
+            auto ml_of = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part_of(c) + 128 * 128 * 4) + r); };
+            float M = kLogitFloor, den = 0.f;
+#pragma unroll 1
+            for (int c = c_first; c <= c_last; ++c) M = fmaxf(M, ml_of(c).x);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {                        // 64 channels at a time
+                float o[2][32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0.f;
+                den = 0.f;
+#pragma unroll 1
+                for (int c = c_first; c <= c_last; ++c) {
+                    const float4* src = reinterpret_cast<const float4*>(part_of(c)) + 16 * h * 128 + r;
+                    float4 v[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[q] = __ldcg(src + q * 128);
+                    const float2 ml = ml_of(c);
+                    const float w = fast_exp2(ml.x - M);         // 0 for a piece that saw no position of the row
+                    den = fmaf(w, ml.y, den);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        float* d = &o[q >> 3][4 * (q & 7)];
+                        d[0] = fmaf(w, v[q].x, d[0]);
+                        d[1] = fmaf(w, v[q].y, d[1]);
+                        d[2] = fmaf(w, v[q].z, d[2]);
+                        d[3] = fmaf(w, v[q].w, d[3]);
+                    }
+                }
+                store_out(2 * h, o[0], 1.f / den);
+                store_out(2 * h + 1, o[1], 1.f / den);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == S::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+}  // namespace pkv

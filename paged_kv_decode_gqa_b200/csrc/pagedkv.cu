@@ -22,6 +22,7 @@
 #include "prefill_tc.cuh"
 #include "int8_cache.cuh"
 #include "stream_int8.cuh"
+#include "chunk_int8_tc.cuh"
 
 namespace {
 
@@ -776,9 +777,7 @@ bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 
 // ------------------------------------------- 8-bit cache, rotary cache write
-constexpr int kStreamWarps1 = 12, kStreamStages1 = 3;   // one column tile (decode)
-constexpr int kStreamWarpsN = 8, kStreamStagesN = 3;    // several (short chunks)
-constexpr int kStreamMaxTiles = 4;
+constexpr int kStreamWarps = 12, kStreamStages = 3;
 
 // kv_scales [NB, Hkv, 2, 16] fp32 as a 3-D tensor (32 scales, head, block), one
 // box = the 32 scales of a page and head; blocks outside the pool read zeros.
@@ -823,58 +822,47 @@ int device_sms() {
     return sms;
 }
 
-// Workspace of the streaming kernel for `tiles` column tiles: the merge tickets
-// first, at the same place whatever the plan (they are zero between calls, so
-// calls of every plan can share a workspace), then (m, l) and O of two pieces
-// per worker warp.
-struct StreamWorkspace {
-    size_t tickets, ml, o, total;
+// Workspace of the 8-bit attention kernels: the merge tickets first, at the
+// same place whatever the kernel (they are zero between calls, so calls of
+// every kind can share a workspace), then the pieces' partial results: (m, l)
+// and O of two pieces per worker warp (streaming), or of two pieces x two
+// softmax streams per CTA (tensor-core chunks).
+struct Int8Workspace {
+    size_t tickets, ml, o, stream_total, parts, total;
 };
-StreamWorkspace stream_workspace(int sms, int tiles) {
-    const size_t slots = 2 * (size_t)sms * (tiles == 1 ? kStreamWarps1 : kStreamWarpsN);
-    StreamWorkspace w;
+Int8Workspace int8_workspace(int sms) {
+    const size_t slots = 2 * (size_t)sms * kStreamWarps;
+    Int8Workspace w;
     w.tickets = 0;
-    w.ml = align256(pkv::kMergeLevels * 2 * (size_t)sms * std::max(kStreamWarps1, kStreamWarpsN) * sizeof(unsigned int));
-    w.o = w.ml + align256(slots * tiles * 4 * sizeof(float4));
-    w.total = w.o + slots * tiles * 256 * sizeof(float4);
+    w.ml = align256(pkv::kMergeLevels * slots * sizeof(unsigned int));
+    static_assert(pkv::kMergeLevels * 2 * kStreamWarps >= 2 * 4, "tickets of a CTA's two streams x four warps fit");
+    w.o = w.ml + align256(slots * 4 * sizeof(float4));
+    w.stream_total = w.o + slots * 256 * sizeof(float4);
+    w.parts = w.ml;
+    w.total = std::max(w.stream_total, w.parts + 2 * (size_t)sms * 2 * pkv::ChunkInt8Shape::kPartBytes);
     return w;
 }
 
-// Column tiles of a chunk call: enough for the longest chunk's (query, head)
-// columns, at most kStreamMaxTiles (longer chunks take several query groups).
-int stream_tiles(int max_query_len, int G) {
-    return (int)std::min<int64_t>(kStreamMaxTiles, ((int64_t)max_query_len * G + 7) / 8);
+// The workspace pointer and size of a call that needs `need` bytes of it.
+bool workspace_ok(const void* workspace, size_t bytes, size_t need) {
+    return workspace && bytes >= need && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0;
 }
 
-template <int kNT>
-pkv_status launch_stream_int8(const pkv::StreamInt8Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
-                              const CUtensorMap& ms, int sms, cudaStream_t st) {
-    constexpr int kWarps = kNT == 1 ? kStreamWarps1 : kStreamWarpsN;
-    constexpr int kStages = kNT == 1 ? kStreamStages1 : kStreamStagesN;
-    using S = pkv::StreamInt8Shape<kNT, kWarps, kStages>;
-    auto kernel = pkv::stream_int8_kernel<kNT, kWarps, kStages>;
-    static unsigned long long done = 0;
-    if (ensure_smem(kernel, (int)S::smem_bytes(kBalMaxBatch), &done) != cudaSuccess) return PKV_ERR_CUDA;
-    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::kThreads), S::smem_bytes(prm.B), st, mk, mv, ms, prm) ==
-                   cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+// Whether the streaming kernel can number the units of this batch.
+bool stream_fits(int64_t B, int64_t Hkv, int64_t max_context_len) {
+    const int64_t pages = std::max<int64_t>(1, (max_context_len + kPageRows - 1) / kPageRows);
+    return B <= kBalMaxBatch && B * Hkv <= INT32_MAX / pages;
 }
 
-// Decode (query_start null) and short chunks over the 8-bit cache.
-pkv_status stream_int8(pkv::StreamInt8Params prm, const void* k_cache, const void* v_cache, const float* kv_scales,
-                       void* workspace, size_t workspace_bytes, cudaStream_t st) {
-    const bool chunked = prm.query_start != nullptr;
-    const int tiles = chunked ? stream_tiles(prm.max_query_len, prm.G) : 1;
-    prm.queries_per_group = chunked ? 8 * tiles / prm.G : 1;
+// Decode (query_start null), and chunks whose (query, head) columns fit one
+// product tile of 8, over the 8-bit cache.
+pkv_status launch_stream_int8(pkv::StreamInt8Params prm, const void* k_cache, const void* v_cache,
+                              const float* kv_scales, void* workspace, size_t workspace_bytes, cudaStream_t st) {
     prm.min_units_per_worker = kBalMinUnits;
-    // units of the batch are numbered in 32 bits
-    const int64_t groups = chunked ? (prm.max_query_len + prm.queries_per_group - 1) / prm.queries_per_group : 1;
-    const int64_t pages = std::max(1, (prm.max_context_len + kPageRows - 1) / kPageRows);
-    if (prm.B > kBalMaxBatch || (int64_t)prm.B * prm.Hkv * groups > INT32_MAX / pages) return PKV_ERR_UNSUPPORTED;
     const int sms = device_sms();
     if (sms <= 0) return PKV_ERR_CUDA;
-    const StreamWorkspace w = stream_workspace(sms, tiles);
-    if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return PKV_ERR_WORKSPACE;
+    const Int8Workspace w = int8_workspace(sms);
+    if (!workspace_ok(workspace, workspace_bytes, w.stream_total)) return PKV_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     prm.ws_count = reinterpret_cast<unsigned int*>(ws + w.tickets);
     prm.ws_ml = reinterpret_cast<float4*>(ws + w.ml);
@@ -884,12 +872,45 @@ pkv_status stream_int8(pkv::StreamInt8Params prm, const void* k_cache, const voi
         !cached_cache_map(&mv, v_cache, true, prm.num_blocks, prm.Hkv) ||
         !cached_scale_map(&ms, kv_scales, prm.num_blocks, prm.Hkv))
         return PKV_ERR_CUDA;
-    switch (tiles) {
-        case 1: return launch_stream_int8<1>(prm, mk, mv, ms, sms, st);
-        case 2: return launch_stream_int8<2>(prm, mk, mv, ms, sms, st);
-        case 3: return launch_stream_int8<3>(prm, mk, mv, ms, sms, st);
-        default: return launch_stream_int8<4>(prm, mk, mv, ms, sms, st);
-    }
+    using S = pkv::StreamInt8Shape<kStreamWarps, kStreamStages>;
+    auto kernel = pkv::stream_int8_kernel<kStreamWarps, kStreamStages>;
+    static unsigned long long done = 0;
+    if (ensure_smem(kernel, (int)S::smem_bytes(kBalMaxBatch), &done) != cudaSuccess) return PKV_ERR_CUDA;
+    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::kThreads), S::smem_bytes(prm.B), st, mk, mv, ms, prm) ==
+                   cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// Chunks on tcgen05: narrow when the longest fits one query tile.
+template <bool kNarrow>
+cudaError_t launch_chunk(int sms, cudaStream_t st, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                         const CUtensorMap& ms, const pkv::ChunkInt8Params& prm) {
+    using S = pkv::ChunkInt8Shape;
+    auto kernel = pkv::chunk_int8_kernel<kNarrow>;
+    static unsigned long long done = 0;
+    const cudaError_t e = ensure_smem(kernel, S::kSmemBytes, &done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::kThreads), S::kSmemBytes, st, mq, mk, mv, ms, prm);
+}
+
+pkv_status launch_chunk_int8(pkv::ChunkInt8Params prm, const void* q, const void* k_cache, const void* v_cache,
+                             const float* kv_scales, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+    const int sms = device_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const Int8Workspace w = int8_workspace(sms);
+    if (!workspace_ok(workspace, workspace_bytes, w.total)) return PKV_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    prm.tickets = reinterpret_cast<unsigned int*>(ws + w.tickets);
+    prm.parts = ws + w.parts;
+    prm.tokens = 128 / prm.G;
+    CUtensorMap mq, mk, mv, ms;
+    if (!make_q_map(&mq, q, prm.Hq, prm.total, prm.G, prm.tokens) ||
+        !cached_cache_map(&mk, k_cache, true, prm.num_blocks, prm.Hkv) ||
+        !cached_cache_map(&mv, v_cache, true, prm.num_blocks, prm.Hkv) ||
+        !cached_scale_map(&ms, kv_scales, prm.num_blocks, prm.Hkv))
+        return PKV_ERR_CUDA;
+    const cudaError_t e = prm.max_query_len <= prm.tokens ? launch_chunk<true>(sms, st, mq, mk, mv, ms, prm)
+                                                          : launch_chunk<false>(sms, st, mq, mk, mv, ms, prm);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 // Arguments shared by the cache write with rotation (or without: half = 0) and
@@ -1191,7 +1212,7 @@ size_t paged_gqa_prefill_workspace_size(int32_t num_q_heads, int32_t num_kv_head
     if (kv_dtype == PKV_KV_FP8_E4M3) return 0;                  // the warp-level FP8 kernel takes none
     if (kv_dtype == PKV_KV_INT8) {
         const int n = device_sms();
-        return n > 0 ? std::max(stream_workspace(n, 1).total, stream_workspace(n, kStreamMaxTiles).total) : 0;
+        return n > 0 ? int8_workspace(n).total : 0;
     }
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1402,7 +1423,7 @@ pkv_status paged_kv_cache_read(void* k_out, void* v_out, const void* k_cache, co
 
 size_t paged_gqa_decode_workspace_size_int8(void) {
     const int sms = device_sms();
-    return sms > 0 ? stream_workspace(sms, 1).total : 0;
+    return sms > 0 ? int8_workspace(sms).stream_total : 0;
 }
 
 pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1417,6 +1438,7 @@ pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void*
                                               max_context_len, softmax_scale, PKV_KV_F16, 1.f, 1.f, 0);
     if (v != PKV_OK || batch == 0) return v;
     if (!kv_scales || !aligned16(kv_scales)) return PKV_ERR_INVALID_ARG;
+    if (!stream_fits(batch, num_kv_heads, max_context_len)) return PKV_ERR_UNSUPPORTED;
     pkv::StreamInt8Params prm{};
     prm.out = static_cast<__half*>(out);
     prm.q = static_cast<const __half*>(q);
@@ -1432,7 +1454,8 @@ pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void*
     prm.num_blocks = num_blocks;
     prm.max_context_len = max_context_len;
     prm.logit_scale_log2 = softmax_scale * 1.4426950408889634f;
-    return stream_int8(prm, k_cache, v_cache, kv_scales, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    return launch_stream_int8(prm, k_cache, v_cache, kv_scales, workspace, workspace_bytes,
+                              static_cast<cudaStream_t>(stream));
 }
 
 pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1452,23 +1475,44 @@ pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void
     if (!kv_scales || !aligned16(kv_scales)) return PKV_ERR_INVALID_ARG;
     if (!query_start || (reinterpret_cast<uintptr_t>(query_start) & 3u)) return PKV_ERR_INVALID_ARG;
     if (max_query_len > max_context_len) return PKV_ERR_INVALID_ARG;
-    pkv::StreamInt8Params prm{};
+    const int G = num_q_heads / num_kv_heads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (max_query_len * (int64_t)G <= 8 && stream_fits(batch, num_kv_heads, max_context_len)) {
+        pkv::StreamInt8Params prm{};
+        prm.out = static_cast<__half*>(out);
+        prm.q = static_cast<const __half*>(q);
+        prm.block_tables = block_tables;
+        prm.context_lens = context_lens;
+        prm.query_start = query_start;
+        prm.B = batch;
+        prm.Hq = num_q_heads;
+        prm.Hkv = num_kv_heads;
+        prm.G = G;
+        prm.total = total_queries;
+        prm.max_query_len = max_query_len;
+        prm.max_blocks_per_seq = max_blocks_per_seq;
+        prm.num_blocks = num_blocks;
+        prm.max_context_len = max_context_len;
+        prm.logit_scale_log2 = softmax_scale * 1.4426950408889634f;
+        return launch_stream_int8(prm, k_cache, v_cache, kv_scales, workspace, workspace_bytes, st);
+    }
+    pkv::ChunkInt8Params prm{};
     prm.out = static_cast<__half*>(out);
-    prm.q = static_cast<const __half*>(q);
     prm.block_tables = block_tables;
     prm.context_lens = context_lens;
     prm.query_start = query_start;
-    prm.B = batch;
-    prm.Hq = num_q_heads;
-    prm.Hkv = num_kv_heads;
-    prm.G = num_q_heads / num_kv_heads;
+    prm.batch = batch;
     prm.total = total_queries;
     prm.max_query_len = max_query_len;
+    prm.Hq = num_q_heads;
+    prm.Hkv = num_kv_heads;
+    prm.G = G;
     prm.max_blocks_per_seq = max_blocks_per_seq;
     prm.num_blocks = num_blocks;
     prm.max_context_len = max_context_len;
-    prm.logit_scale_log2 = softmax_scale * 1.4426950408889634f;
-    return stream_int8(prm, k_cache, v_cache, kv_scales, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    prm.logit_scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
+    prm.key_sign = softmax_scale < 0.f ? -1.f : 1.f;
+    return launch_chunk_int8(prm, q, k_cache, v_cache, kv_scales, workspace, workspace_bytes, st);
 }
 
 }  // extern "C"
