@@ -28,8 +28,7 @@
 //    token's scale is a register: a code becomes an exact f16 integer (a byte
 //    permute and a subtraction), and code * scale is formed in f16x2 as
 //    code * hi + (code * lo) with scale = hi + lo split into two f16, which
-//    leaves one rounding (rows whose scale is below 2^-12, where lo would be
-//    subnormal, go through fp32). The f16 tiles are written in the 128-byte
+//    leaves one rounding (RowScale). The f16 tiles are written in the 128-byte
 //    swizzled layout the tensor cores read: K and V are double-buffered.
 //    Codes are finite and rows past the context get scale 0, so no row needs
 //    clearing.
@@ -87,19 +86,40 @@ struct ChunkInt8Shape {
     static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
 };
 
-// Four codes to four f16 of code * (hi + lo), rounded once (to within 2^-22).
-__device__ __forceinline__ void dequant4(uint32_t w, __half2 hi, __half2 lo, uint32_t& d0, uint32_t& d1) {
+// A token's scale for the conversion: scale = (hi + lo) * post, hi and lo f16. post is 1 unless the
+// scale is small (below 2^-12, where lo would lose bits to the subnormal range): then hi + lo is the
+// scale brought into [2^-7, 2^-6) and post the power of two that takes it back.
+struct RowScale {
+    __half2 hi, lo, post;
+    bool small;
+};
+__device__ __forceinline__ RowScale split_scale(float s) {
+    RowScale r;
+    r.small = fabsf(s) < 2.44140625e-4f && s != 0.f;
+    float post = 1.f;
+    if (r.small) {
+        const int e = max((int)((__float_as_uint(s) >> 23) & 0xff) - 127 + 7, -24);   // post = 2^e >= 2^-24
+        post = __uint_as_float((uint32_t)(e + 127) << 23);
+        s *= __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+    const __half hi = __float2half_rn(s);
+    r.hi = __half2half2(hi);
+    r.lo = __half2half2(__float2half_rn(s - __half2float(hi)));
+    r.post = __half2half2(__float2half_rn(post));
+    return r;
+}
+// Four codes to four f16 of code * (hi + lo), rounded once (to within 2^-18 of a step).
+__device__ __forceinline__ void dequant4(uint32_t w, const RowScale& s, uint32_t& d0, uint32_t& d1) {
     uint32_t a, b;
     codes_to_half2x2(w, a, b);
     const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&b);
-    const __half2 u = __hfma2(x, hi, __hmul2(x, lo)), v = __hfma2(y, hi, __hmul2(y, lo));
+    const __half2 u = __hfma2(x, s.hi, __hmul2(x, s.lo)), v = __hfma2(y, s.hi, __hmul2(y, s.lo));
     d0 = *reinterpret_cast<const uint32_t*>(&u);
     d1 = *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void dequant4_small(uint32_t w, float s, uint32_t& d0, uint32_t& d1) {
-    auto f = [&](int k) { return (float)((int)((w >> (8 * k)) & 0xff) - 128) * s; };
-    d0 = pack_half2(f(0), f(1));
-    d1 = pack_half2(f(2), f(3));
+__device__ __forceinline__ uint32_t times(uint32_t a, __half2 f) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <bool kNarrow>
@@ -419,35 +439,34 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // ========================= codes to f16 tiles: a token per thread =========================
         const int row = 32 * (warp - S::kConvertWarp) + lane;      // token of the KV tile
         const uint32_t sw = (uint32_t)(row & 7);
-        // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`
-        auto convert = [&](uint32_t src, uint32_t dst, float s) {
-            const float a = fabsf(s);
-            const bool small = a < 2.44140625e-4f;                 // 2^-12; 0 included
-            const __half hi = __float2half_rn(s);
-            const __half lo = __float2half_rn(s - __half2float(hi));
-            const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+        // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`, 64 channels at
+        // a time (kept as a loop: the roles' code competes for the instruction cache)
+        auto convert = [&](uint32_t src, uint32_t dst, float scale) {
+            const RowScale s = split_scale(scale);
+            const bool any_small = __any_sync(0xffffffffu, s.small);
             const uint32_t in = src + row * 128, out = dst + row * 128;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                uint4 w[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {                          // 16 channels a step
-                const uint4 w = lds128(in + ((c ^ sw) << 4));
-                uint32_t d[8];
-                if (!small) {
-                    dequant4(w.x, hi2, lo2, d[0], d[1]);
-                    dequant4(w.y, hi2, lo2, d[2], d[3]);
-                    dequant4(w.z, hi2, lo2, d[4], d[5]);
-                    dequant4(w.w, hi2, lo2, d[6], d[7]);
-                } else {
-                    dequant4_small(w.x, s, d[0], d[1]);
-                    dequant4_small(w.y, s, d[2], d[3]);
-                    dequant4_small(w.z, s, d[4], d[5]);
-                    dequant4_small(w.w, s, d[6], d[7]);
+                for (int c = 0; c < 4; ++c) w[c] = lds128(in + (((4 * h + c) ^ sw) << 4));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {                      // 16 channels
+                    uint32_t d[8];
+                    dequant4(w[c].x, s, d[0], d[1]);
+                    dequant4(w[c].y, s, d[2], d[3]);
+                    dequant4(w[c].z, s, d[4], d[5]);
+                    dequant4(w[c].w, s, d[6], d[7]);
+                    if (any_small) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d[e] = times(d[e], s.post);
+                    }
+                    const uint32_t o = out + h * S::kChunk;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(o + (((2 * c) ^ sw) << 4)), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(o + (((2 * c + 1) ^ sw) << 4)), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]) : "memory");
                 }
-                const uint32_t o = out + (c >> 2) * S::kChunk;
-                const uint32_t c0 = (uint32_t)(2 * (c & 3));
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                             :: "r"(o + ((c0 ^ sw) << 4)), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                             :: "r"(o + (((c0 + 1) ^ sw) << 4)), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]) : "memory");
             }
         };
         // the row's scale: 0 past the context; outside [0, 2^60] flagged and 0; saturating at the f16 range
@@ -463,43 +482,32 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         Piece pc;
         int gj = 0;                                                // KV tiles of earlier pieces
         float v_scale[2] = {0.f, 0.f};                             // of the tiles whose K is converted, V not yet
-        auto do_k = [&](int i) -> bool {
-            const int g = gj + i, s = g % kRawStages, d = g & 1;
-            if (!wait_all(rk_full(s), (g / kRawStages) & 1)) return false;
-            const float ks = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
-            const float vs = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
-            if (d) v_scale[1] = vs;
-            else v_scale[0] = vs;
-            if (g >= 2 && !wait_all(k_empty(d), ((g >> 1) - 1) & 1)) return false;
-            convert(raw_k(s), k_s(d), ks);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(rk_empty(s));
-                mbar_arrive(k_full(d));
-            }
-            return true;
-        };
-        auto do_v = [&](int i) -> bool {
-            const int g = gj + i, s = g % kRawStages, d = g & 1;
-            if (!wait_all(rv_full(s), (g / kRawStages) & 1)) return false;
-            if (g >= 2 && !wait_all(v_empty(d), ((g >> 1) - 1) & 1)) return false;
-            convert(raw_v(s), v_s(d), d ? v_scale[1] : v_scale[0]);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(rv_empty(s));
-                mbar_arrive(v_full(d));
-            }
-            return true;
-        };
         bool ok = true;
-        while (ok && next_piece(cu, pc)) {                         // K runs one tile ahead of V
+        while (ok && next_piece(cu, pc)) {
+            // steps K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
             const int n = pc.j1 - pc.j0;
-            ok = do_k(0);
-            for (int i = 0; ok && i < n; ++i) {
-                if (i + 1 < n) ok = do_k(i + 1);
-                if (ok) ok = do_v(i);
+            for (int step = 0; step < 2 * n; ++step) {
+                const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
+                const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
+                const int g = gj + i, s = g % kRawStages, d = g & 1;
+                if (!(ok = wait_all(is_k ? rk_full(s) : rv_full(s), (g / kRawStages) & 1))) break;
+                float scale;
+                if (is_k) {
+                    scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
+                    const float vs = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
+                    if (d) v_scale[1] = vs;
+                    else v_scale[0] = vs;
+                } else {
+                    scale = d ? v_scale[1] : v_scale[0];
+                }
+                if (g >= 2 && !(ok = wait_all(is_k ? k_empty(d) : v_empty(d), ((g >> 1) - 1) & 1))) break;
+                convert(is_k ? raw_k(s) : raw_v(s), is_k ? k_s(d) : v_s(d), scale);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(is_k ? rk_empty(s) : rv_empty(s));
+                    mbar_arrive(is_k ? k_full(d) : v_full(d));
+                }
             }
             gj += n;
         }
