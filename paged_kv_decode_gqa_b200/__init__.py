@@ -439,76 +439,77 @@ def paged_gqa_prefill_attention(out, q, k_cache, v_cache, block_tables, context_
 # The 8-bit cache (a scale per token and KV head), rotary positions with the
 # cache write, and reading a cache back.
 
-def _here(*tensors):
-    """Checks that the tensors are on the current device: launches go to its current stream."""
-    import torch
-    for t in tensors:
-        if t is not None and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+# These calls sit in a decode step's inner loop, where the host's time counts: a tensor is checked by
+# one comparison of its attributes, and the reason is worked out only when that fails.
+
+def _refuse(name, t, dtype, shape, device):
+    _dense(name, t, str(dtype).replace("torch.", ""))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
 
 
-def _shapes(**named):
-    """Checks (tensor, shape) pairs given by name."""
-    for name, (t, shape) in named.items():
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _take(name, t, dtype, shape, device):
+    """The address of `t`, a dense tensor of this type and shape on the current device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, device)
+    return t.data_ptr()
 
 
-def _cache(k_cache, v_cache, kv_dtype, kv_scales=None):
-    """Checks a cache of any type; its (num_blocks, block_size, Hkv, D) and type code."""
-    if kv_dtype not in _CACHE_DTYPES:
+def _raw_stream(stream, torch, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device):
+    """Checks a cache of any type: its addresses (K, V, scales), its sizes and its type code."""
+    code = _CACHE_DTYPES.get(kv_dtype)
+    if code is None:
         raise ValueError(f"kv_dtype must be one of {sorted(_CACHE_DTYPES)}")
-    dtype = "float16" if kv_dtype == "f16" else "uint8"
-    _dense("k_cache", k_cache, dtype)
-    _dense("v_cache", v_cache, dtype)
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
-    NB, bs, Hkv, D = k_cache.shape
-    _shapes(v_cache=(v_cache, k_cache.shape))
-    if kv_dtype == "int8":
+    dtype = torch.float16 if code == PKV_KV_F16 else torch.uint8
+    kc, vc = _take("k_cache", k_cache, dtype, shape, device), _take("v_cache", v_cache, dtype, shape, device)
+    NB, bs, Hkv, D = shape
+    sc = None
+    if code == PKV_KV_INT8:
         if kv_scales is None:
             raise ValueError("an int8 cache needs kv_scales")
-        _dense("kv_scales", kv_scales, "float32")
-        _shapes(kv_scales=(kv_scales, (NB, Hkv, 2, bs)))
+        sc = _take("kv_scales", kv_scales, torch.float32, (NB, Hkv, 2, bs), device)
     elif kv_scales is not None:
         raise ValueError("kv_scales belongs to an int8 cache")
-    _here(k_cache, v_cache, kv_scales)
-    return NB, bs, Hkv, D, _CACHE_DTYPES[kv_dtype]
-
-
-def _rows(name, t, T, H, D):
-    _dense(name, t, "float16")
-    _shapes(**{name: (t, (T, H, D))})
-    _here(t)
+    return kc, vc, sc, NB, bs, Hkv, D, code
 
 
 def paged_kv_cache_write_int8(k_new, v_new, k_cache, v_cache, kv_scales, slot_mapping, *, stream=None) -> None:
     """paged_kv_cache_write into an 8-bit cache: codes 128 + round(x / s) (uint8) and, in
     kv_scales [NB, Hkv, 2, 16] float32, s = max(max|x|, 2**-24) / 127 of every token and KV head."""
-    NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales)
-    _dense("slot_mapping", slot_mapping, "int64")
+    import torch
+    device = torch.cuda.current_device()
+    kc, vc, sc, NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales, torch, device)
     T = slot_mapping.numel()
-    _rows("k_new", k_new, T, Hkv, D)
-    _rows("v_new", v_new, T, Hkv, D)
-    _here(slot_mapping)
-    _check(load_library().paged_kv_cache_write_int8(
-        _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(slot_mapping), T, Hkv, D, NB,
-        bs, _stream(stream)), "paged_kv_cache_write_int8")
+    rows = (T, Hkv, D)
+    _check((_lib or load_library()).paged_kv_cache_write_int8(
+        _take("k_new", k_new, torch.float16, rows, device), _take("v_new", v_new, torch.float16, rows, device),
+        kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
+        _raw_stream(stream, torch, device)), "paged_kv_cache_write_int8")
 
 
 def paged_kv_cache_read(k_out, v_out, k_cache, v_cache, slot_mapping, *, kv_dtype="f16", kv_scales=None,
                         k_scale=1.0, v_scale=1.0, stream=None) -> None:
     """k_out[i], v_out[i] ([T, Hkv, D] float16) = the cached values of slot slot_mapping[i], for an
     "f16", "fp8" or "int8" cache. Rows of negative slots are left as they were."""
-    NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales)
-    _dense("slot_mapping", slot_mapping, "int64")
+    import torch
+    device = torch.cuda.current_device()
+    kc, vc, sc, NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device)
     T = slot_mapping.numel()
-    _rows("k_out", k_out, T, Hkv, D)
-    _rows("v_out", v_out, T, Hkv, D)
-    _here(slot_mapping)
-    _check(load_library().paged_kv_cache_read(
-        _ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(slot_mapping), T, Hkv, D, NB,
-        bs, code, float(k_scale), float(v_scale), _stream(stream)), "paged_kv_cache_read")
+    rows = (T, Hkv, D)
+    _check((_lib or load_library()).paged_kv_cache_read(
+        _take("k_out", k_out, torch.float16, rows, device), _take("v_out", v_out, torch.float16, rows, device),
+        kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
+        code, k_scale, v_scale, _raw_stream(stream, torch, device)), "paged_kv_cache_read")
 
 
 def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq, *,
@@ -523,40 +524,39 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
     (j, j + rotary_dim / 2). For an "fp8" cache k_scale and v_scale are numbers, or float32 CUDA
     tensors of 1 or Hkv elements.
     """
-    NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales)
-    _dense("slot_mapping", slot_mapping, "int64")
-    _dense("positions", positions, "int64")
-    _dense("inv_freq", inv_freq, "float32")
+    import torch
+    device = torch.cuda.current_device()
+    kc, vc, sc, NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device)
     T = slot_mapping.numel()
-    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
-        raise ValueError(f"positions must be [{T}] or [axes, {T}], got {tuple(positions.shape)}")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
+    where = positions.shape
+    axes = where[0] if len(where) == 2 else 1
+    if len(where) not in (1, 2) or where[-1] != T:
+        raise ValueError(f"positions must be [{T}] or [axes, {T}], got {tuple(where)}")
     half = inv_freq.numel()
-    sections = [half] if sections is None else [int(n) for n in sections]
+    sections = (half,) if sections is None else sections
     if len(sections) != axes:
         raise ValueError(f"{len(sections)} sections for {axes} position axes")
     if q.dim() != 3:
         raise ValueError("q must be [T, num_q_heads, head_dim]")
     Hq = q.shape[1]
-    _rows("q", q, T, Hq, D)
-    _rows("q_out", q_out, T, Hq, D)
-    _rows("k_new", k_new, T, Hkv, D)
-    _rows("v_new", v_new, T, Hkv, D)
-    _here(slot_mapping, positions, inv_freq)
+    rows, kv_rows = (T, Hq, D), (T, Hkv, D)
     flags = (PKV_ROPE_INTERLEAVED if interleaved else 0) | (PKV_ROPE_CYCLIC_AXES if cyclic_axes else 0)
-    host_sections = (ctypes.c_int32 * max(axes, 1))(*sections)
-    head = (_ptr(q_out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache))
-    sizes = (_ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), T, Hq, Hkv, D, 2 * half, axes, host_sections, NB, bs)
-    if kv_dtype == "fp8" and hasattr(k_scale, "data_ptr"):
+    f16, lib, st = torch.float16, _lib or load_library(), _raw_stream(stream, torch, device)
+    head = (_take("q_out", q_out, f16, rows, device), _take("q", q, f16, rows, device),
+            _take("k_new", k_new, f16, kv_rows, device), _take("v_new", v_new, f16, kv_rows, device), kc, vc)
+    sizes = (_take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device),
+             _take("positions", positions, torch.int64, where, device),
+             _take("inv_freq", inv_freq, torch.float32, inv_freq.shape, device),
+             T, Hq, Hkv, D, 2 * half, axes, (_i32 * max(axes, 1))(*sections), NB, bs)
+    if code == PKV_KV_FP8_E4M3 and hasattr(k_scale, "data_ptr"):
         per_head = _scales(k_scale, v_scale, Hkv)
-        _here(k_scale, v_scale)
-        _check(load_library().paged_kv_rope_cache_write_fp8_scaled(
-            *head, *sizes, _ptr(k_scale), _ptr(v_scale), per_head, flags, _stream(stream)),
+        _check(lib.paged_kv_rope_cache_write_fp8_scaled(
+            *head, *sizes, _take("k_scales", k_scale, torch.float32, k_scale.shape, device),
+            _take("v_scales", v_scale, torch.float32, v_scale.shape, device), per_head, flags, st),
             "paged_kv_rope_cache_write_fp8_scaled")
         return
-    _check(load_library().paged_kv_rope_cache_write(
-        *head, _ptr(kv_scales), *sizes, code, float(k_scale), float(v_scale), flags, _stream(stream)),
-        "paged_kv_rope_cache_write")
+    _check(lib.paged_kv_rope_cache_write(*head, sc, *sizes, code, k_scale, v_scale, flags, st),
+           "paged_kv_rope_cache_write")
 
 
 def paged_gqa_decode_workspace_size_int8() -> int:
@@ -564,34 +564,36 @@ def paged_gqa_decode_workspace_size_int8() -> int:
     return int(load_library().paged_gqa_decode_workspace_size_int8())
 
 
-def _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace):
-    NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales)
+def _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device):
+    """Checks what decode and chunk attention share: the addresses in call order, and the sizes."""
+    kc, vc, sc, NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales, torch, device)
     if q.dim() != 3 or block_tables.dim() != 2:
         raise ValueError("q must be [rows, num_q_heads, head_dim] and block_tables [batch, max_blocks]")
-    rows, Hq, _ = q.shape
-    _rows("q", q, rows, Hq, D)
-    _rows("out", out, rows, Hq, D)
-    _dense("block_tables", block_tables, "int32")
-    _dense("context_lens", context_lens, "int32")
-    _dense("workspace", workspace, "uint8", "float32", "int32")
-    B = block_tables.shape[0]
-    _shapes(context_lens=(context_lens, (B,)))
-    _here(block_tables, context_lens, workspace)
-    return rows, Hq, Hkv, D, NB, bs, B, workspace.numel() * workspace.element_size()
+    n, Hq, _ = q.shape
+    B, mb = block_tables.shape
+    rows = (n, Hq, D)
+    if workspace.dtype is not torch.uint8:
+        _dense("workspace", workspace, "uint8", "float32", "int32")
+    ws = _take("workspace", workspace, workspace.dtype, workspace.shape, device)
+    return ((_take("out", out, torch.float16, rows, device), _take("q", q, torch.float16, rows, device), kc, vc, sc,
+             _take("block_tables", block_tables, torch.int32, (B, mb), device),
+             _take("context_lens", context_lens, torch.int32, (B,), device)),
+            n, Hq, Hkv, D, NB, bs, B, mb, ws, workspace.numel() * workspace.element_size())
 
 
 def paged_gqa_decode_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, *,
                                     max_context_len, softmax_scale, workspace, stream=None) -> None:
     """paged_gqa_decode_attention over an 8-bit cache (load-balanced plan; a zero-filled workspace of
     paged_gqa_decode_workspace_size_int8() bytes, reusable)."""
-    rows, Hq, Hkv, D, NB, bs, B, ws_bytes = _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables,
-                                                            context_lens, workspace)
-    if rows != B:
-        raise ValueError(f"{rows} query rows for {B} sequences")
-    _check(load_library().paged_gqa_decode_attention_int8(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(block_tables), _ptr(context_lens),
-        B, Hq, Hkv, D, bs, block_tables.shape[1], NB, int(max_context_len), float(softmax_scale), _ptr(workspace),
-        ws_bytes, _stream(stream)), "paged_gqa_decode_attention_int8")
+    import torch
+    device = torch.cuda.current_device()
+    args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
+        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
+    if n != B:
+        raise ValueError(f"{n} query rows for {B} sequences")
+    _check((_lib or load_library()).paged_gqa_decode_attention_int8(
+        *args, B, Hq, Hkv, D, bs, mb, NB, max_context_len, softmax_scale, ws, ws_bytes,
+        _raw_stream(stream, torch, device)), "paged_gqa_decode_attention_int8")
 
 
 def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, *,
@@ -599,13 +601,11 @@ def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_
     """paged_gqa_prefill_attention over an 8-bit cache: query rows q [total, Hq, D] of each sequence
     (query_start [B+1] int32), the last n_b tokens of its context, attending causally; a zero-filled
     workspace of paged_gqa_prefill_workspace_size(Hq, Hkv, D, "int8") bytes, reusable."""
-    rows, Hq, Hkv, D, NB, bs, B, ws_bytes = _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables,
-                                                            context_lens, workspace)
-    _dense("query_start", query_start, "int32")
-    _shapes(query_start=(query_start, (B + 1,)))
-    _here(query_start)
-    _check(load_library().paged_gqa_prefill_attention_int8(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scales), _ptr(block_tables), _ptr(context_lens),
-        _ptr(query_start), B, rows, int(max_query_len), Hq, Hkv, D, bs, block_tables.shape[1], NB,
-        int(max_context_len), float(softmax_scale), _ptr(workspace), ws_bytes, _stream(stream)),
+    import torch
+    device = torch.cuda.current_device()
+    args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
+        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
+    _check((_lib or load_library()).paged_gqa_prefill_attention_int8(
+        *args, _take("query_start", query_start, torch.int32, (B + 1,), device), B, n, max_query_len, Hq, Hkv, D, bs,
+        mb, NB, max_context_len, softmax_scale, ws, ws_bytes, _raw_stream(stream, torch, device)),
         "paged_gqa_prefill_attention_int8")
