@@ -12,14 +12,19 @@
 // thread i two 8-channel chunks chosen so that the two channels of every
 // rotated pair meet in one thread (chunks i and i + R/16 of the rotated part R;
 // two consecutive chunks of the part left as it is), so neither pairing style
-// needs a shuffle, and the row's amax takes three. The angles of a token are
-// computed once per block (R/2 of them, against up to Hq + Hkv rows that use
-// them) while the rows' loads are in flight: pos * inv_freq in fp64 (exact: 24
-// significant bits times an integer below 2^29, and within 2^-53 past it),
-// reduced to a fraction of a turn, then the fp32 sincospi. In fp32 a position
-// near 2^20 would leave the fastest angle off by 2^-4 radians.
+// needs a shuffle, and the row's amax takes three. A warp holds rows of one
+// token, four at a time: it computes the token's R/2 angles once (two a lane,
+// exchanged through its own shared memory, while its first rows are in flight),
+// and every thread keeps the eight it needs in registers for all its rows. No
+// block-wide step exists. A token's rows are shared out over several warps only
+// when there are too few tokens to fill the SMs.
+// Angles: pos * inv_freq in fp64 (exact: 24 significant bits times an integer
+// below 2^29, and within 2^-53 past it), reduced to a fraction of a turn, then
+// the fp32 sincospi. In fp32 a position near 2^20 would leave the fastest angle
+// off by 2^-4 radians.
 // Rounding: fp32 throughout, once to f16, to E4M3 (of x / scale, an IEEE
 // division, as paged_kv_cache_write) or to the 8-bit code.
+// Bound: HBM; every row is read and written once.
 #pragma once
 
 #include "cache_write.cuh"
@@ -51,8 +56,26 @@ struct RopeWriteParams {
     const float* k_scales;     // FP8 device scales or null
     const float* v_scales;
     int32_t scales_per_head;
-    int32_t tokens_per_block;
+    int32_t splits;            // warps that share a token's rows
 };
+
+// Four codes (low byte first) to two f16x2 of their exact values: 0x6400 | code
+// is 1024 + code in f16, and 1152 is subtracted exactly.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t h) {
+    const uint32_t bias = 0x64806480u;
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+// bytes (0, 1) and (2, 3): consecutive channels of one token
+__device__ __forceinline__ void codes_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    lo = sub_1152(prmt(w, 0x64646464u, 0x5140u));
+    hi = sub_1152(prmt(w, 0x64646464u, 0x5342u));
+}
+// bytes (0, 2) and (1, 3): one channel of two tokens each
+__device__ __forceinline__ void codes_to_half2x2_cross(uint32_t w, uint32_t& even, uint32_t& odd) {
+    even = sub_1152(prmt(w, 0x64646464u, 0x5240u));
+    odd = sub_1152(prmt(w, 0x64646464u, 0x5341u));
+}
 
 // 16-byte load of data read once. Not through the read-only path: q may be
 // rotated in place (each thread reads its channels before it writes them).
@@ -103,14 +126,36 @@ __device__ __forceinline__ float finite_amax8(const float (&f)[8], float m) {
 }
 
 // Codes 128 + round(x / scale) of eight values: nearest even, infinities at
-// +-127, NaN at 0. The division is IEEE, so that the code is the one its
-// definition names, and not a neighbour at a tie.
-__device__ __forceinline__ uint2 quantize8_int8(const float (&f)[8], float scale) {
-    uint32_t w[2] = {0u, 0u};
+// +-127, NaN at 0; x / scale is the fp32 quotient, correctly rounded.
+// x * (1 / scale) is within 3 x 2^-24 x 128 < 2^-15 of that quotient (three
+// roundings of a value of at most 127), so both round to the same integer
+// unless the product lies within 2^-14 of a tie; only then (two values in
+// 10000, and where x is not finite) is the division done.
+__device__ __forceinline__ uint2 quantize8_int8(const float (&f)[8], float scale, float inv) {
+    uint32_t w[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int c = __float2int_rn(f[k] / scale);          // NaN gives 0, infinities saturate
-        w[k >> 2] |= (uint32_t)(min(127, max(-127, c)) + 128) << (8 * (k & 3));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t c[4];
+        bool safe = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float q = f[4 * h + k] * inv;
+            const float r = q + 12583040.f;                  // 1.5 x 2^23 + 128: the low byte is the code
+            c[k] = __float_as_uint(r);
+            safe = safe && fabsf(q - (r - 12583040.f)) < 0.5f - 6.103515625e-5f;
+        }
+        if (!safe) {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const float x = k == 0 ? f[4 * h] : k == 1 ? f[4 * h + 1] : k == 2 ? f[4 * h + 2] : f[4 * h + 3];
+                const uint32_t v = (uint32_t)(min(127, max(-127, __float2int_rn(x / scale))) + 128);   // NaN: 0
+                if (k == 0) c[0] = v;
+                else if (k == 1) c[1] = v;
+                else if (k == 2) c[2] = v;
+                else c[3] = v;
+            }
+        }
+        w[h] = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
     }
     return make_uint2(w[0], w[1]);
 }
@@ -126,118 +171,170 @@ __device__ __forceinline__ int rope_axis(const RopeWriteParams& p, int j) {
     return a;
 }
 
+constexpr int kRopeWarps = 4;       // warps of a block, each on its own
+constexpr int kRopeBatch = 3;       // rows in flight per thread of the rotating write
+constexpr int kRowBatch = 4;        // and of the plain write and the read
+
+// Stores one head row's eight-thread share (chunks ca, cb as fp32 a, b; as read: ua, ub) of K or V.
 template <int kKind>
-__global__ void __launch_bounds__(512) rope_cache_write_kernel(const RopeWriteParams p) {
-    extern __shared__ float2 s_turn[];                   // [tokens_per_block][half] (cos, sin)
-    const int i = threadIdx.x & 7, group = threadIdx.x >> 3, groups = blockDim.x >> 3;
-    const int rows = p.Hq + 2 * p.Hkv;                   // q heads, k heads, v heads of one token
-    const int t0 = (int)blockIdx.x * p.tokens_per_block;
-    const int nt = min(p.tokens_per_block, p.num_tokens - t0);
+__device__ __forceinline__ void store_kv_row(const RopeWriteParams& p, int i, int ca, int cb, bool is_v, int h,
+                                             int64_t slot, bool live, const float (&a)[8], const float (&b)[8],
+                                             const uint4& ua, const uint4& ub) {
+    float scale = 1.f;
+    if constexpr (kKind == kCacheInt8) {             // amax of the row, over its eight threads
+        float m = finite_amax8(b, finite_amax8(a, 0.f));
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        scale = fmaxf(m, kInt8MinAmax) / 127.f;
+    }
+    if (!live || slot < 0) return;                   // padding token
+    if (slot >= p.num_slots) {
+        if (i == 0 && h == 0) flag_error(PKV_DEVERR_SLOT);
+        return;
+    }
+    const int64_t dst = (slot * p.Hkv + h) * 16;     // in chunks of 8 channels
+    void* cache = is_v ? p.v_cache : p.k_cache;
+    if constexpr (kKind == kCacheF16) {
+        reinterpret_cast<uint4*>(cache)[dst + ca] = is_v ? ua : pack8(a);
+        reinterpret_cast<uint4*>(cache)[dst + cb] = is_v ? ub : pack8(b);
+    } else if constexpr (kKind == kCacheFp8) {
+        float s = is_v ? p.v_scale : p.k_scale;
+        if (p.k_scales) s = head_scale(is_v ? p.v_scales : p.k_scales, p.scales_per_head, h);
+        reinterpret_cast<uint2*>(cache)[dst + ca] = quantize8_e4m3_f32(a, s);
+        reinterpret_cast<uint2*>(cache)[dst + cb] = quantize8_e4m3_f32(b, s);
+    } else {
+        const float inv = 1.f / scale;
+        reinterpret_cast<uint2*>(cache)[dst + ca] = quantize8_int8(a, scale, inv);
+        reinterpret_cast<uint2*>(cache)[dst + cb] = quantize8_int8(b, scale, inv);
+        if (i == 0) p.kv_scales[((slot / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot % 16] = scale;
+    }
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const RopeWriteParams p) {
+    __shared__ float2 s_turn[kRopeWarps][64];            // (cos, sin) of the warp's token
+    const int lane = threadIdx.x & 31, i = lane & 7, sub = lane >> 3;
+    const int64_t warp = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    const int tok = (int)(warp / p.splits), split = (int)(warp - (int64_t)tok * p.splits);
+    const int rows = p.Hq + 2 * p.Hkv;                   // q heads, k heads, v heads
     const int rot = p.half >> 3;                         // threads of a row that hold rotated pairs
-    // this thread's two chunks of a rotated row
-    const int ca = i < rot ? i : 2 * i, cb = i < rot ? i + rot : 2 * i + 1;
+    const int ca = i < rot ? i : 2 * i, cb = i < rot ? i + rot : 2 * i + 1;   // this thread's chunks
 
     grid_dependency_wait();
     grid_dependents_launch();
     if (kKind == kCacheFp8 && p.k_scales && blockIdx.x == 0)
         check_scales(p.k_scales, p.v_scales, p.scales_per_head ? p.Hkv : 1, threadIdx.x, blockDim.x);
+    if (tok >= p.num_tokens) return;
 
-    auto source = [&](int t, int row) -> const uint4* {
-        const __half* s = row < p.Hq ? p.q + ((int64_t)t * p.Hq + row) * 128
-                          : row < p.Hq + p.Hkv ? p.k_new + ((int64_t)t * p.Hkv + (row - p.Hq)) * 128
-                                               : p.v_new + ((int64_t)t * p.Hkv + (row - p.Hq - p.Hkv)) * 128;
-        return reinterpret_cast<const uint4*>(s);
-    };
-    uint4 ua, ub;
-    auto load = [&](int item) {
-        if (item < nt * rows) {
-            const int t = item / rows;
-            const uint4* s = source(t0 + t, item - t * rows);
-            ua = ld_once_16(s + ca);
-            ub = ld_once_16(s + cb);
-        }
-    };
-    load(group);                                         // in flight while the angles are computed
-    for (int k = threadIdx.x; k < nt * p.half; k += blockDim.x) {
-        const int t = k / p.half, j = k - t * p.half;
-        const int64_t pos = __ldg(p.positions + (int64_t)rope_axis(p, j) * p.num_tokens + t0 + t);
-        const double turns = (double)pos * (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
-        const float frac = (float)(turns - rint(turns));     // in [-1/2, 1/2]
-        float2 cs;
-        sincospif(2.f * frac, &cs.y, &cs.x);
-        s_turn[k] = cs;
-    }
-    __syncthreads();
-
-    const int last = (nt * rows + groups - 1) / groups * groups;    // whole warps reach the shuffles
-    for (int item = group; item < last; item += groups) {
-        const bool live = item < nt * rows;
-        const int t = live ? item / rows : 0, row = live ? item - t * rows : 0;
-        const int tok = t0 + t;
-        float a[8], b[8];
-        const uint4 va = ua, vb = ub;
-        unpack8(va, a);
-        unpack8(vb, b);
-        load(item + groups);
-        const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
-        if (live && !is_v && i < rot) {
-            const float2* turn = s_turn + t * p.half;
-            if (p.pairs) {                               // channels (2j, 2j + 1): both in one chunk
+    // rows 4 (split + splits k) + sub, k = 0, 1, ...
+    const int stride = 4 * p.splits;
+    uint4 ua[kRopeBatch], ub[kRopeBatch];
+    auto load = [&](int row0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x = turn[4 * ca + k], y = turn[4 * cb + k];
-                    const float a0 = a[2 * k], a1 = a[2 * k + 1], b0 = b[2 * k], b1 = b[2 * k + 1];
-                    a[2 * k] = fmaf(a0, x.x, -a1 * x.y);
-                    a[2 * k + 1] = fmaf(a1, x.x, a0 * x.y);
-                    b[2 * k] = fmaf(b0, y.x, -b1 * y.y);
-                    b[2 * k + 1] = fmaf(b1, y.x, b0 * y.y);
-                }
-            } else {                                     // channels (j, j + R/2): one in each chunk
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 x = turn[8 * i + k];
-                    const float a0 = a[k], b0 = b[k];
-                    a[k] = fmaf(a0, x.x, -b0 * x.y);
-                    b[k] = fmaf(b0, x.x, a0 * x.y);
-                }
+        for (int u = 0; u < kRopeBatch; ++u) {
+            const int row = row0 + u * stride;
+            if (row < rows) {
+                const __half* s = row < p.Hq ? p.q + ((int64_t)tok * p.Hq + row) * 128
+                                  : row < p.Hq + p.Hkv ? p.k_new + ((int64_t)tok * p.Hkv + (row - p.Hq)) * 128
+                                                       : p.v_new + ((int64_t)tok * p.Hkv + (row - p.Hq - p.Hkv)) * 128;
+                ua[u] = ld_once_16(reinterpret_cast<const uint4*>(s) + ca);
+                ub[u] = ld_once_16(reinterpret_cast<const uint4*>(s) + cb);
             }
         }
-        float scale = 1.f;
-        if constexpr (kKind == kCacheInt8) {             // amax of the row, over its eight threads
-            float m = finite_amax8(b, finite_amax8(a, 0.f));
+    };
+    load(4 * split + sub);
+    const int64_t slot = __ldg(p.slot_mapping + tok);
+    float2* turn = s_turn[threadIdx.x >> 5];
+    for (int j = lane; j < p.half; j += 32) {
+        const int64_t pos = __ldg(p.positions + (int64_t)rope_axis(p, j) * p.num_tokens + tok);
+        const double turns = (double)pos * (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
+        const float frac = (float)(turns - rint(turns));     // in [-1/2, 1/2]
+        sincospif(2.f * frac, &turn[j].y, &turn[j].x);
+    }
+    __syncwarp();
+    // pair k of this thread: channels (2k, 2k + 1) of chunk a, then of chunk b; or channel k of both chunks
+    float2 cs[8];
+    if (i < rot) {
 #pragma unroll
-            for (int off = 1; off < 8; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            scale = fmaxf(m, kInt8MinAmax) / 127.f;
+        for (int k = 0; k < 8; ++k) cs[k] = turn[p.pairs ? (k < 4 ? 4 * ca + k : 4 * cb + k - 4) : 8 * i + k];
+    }
+    for (int quad = 4 * split; quad < rows; quad += kRopeBatch * stride) {
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; ++u) {
+            const int first = quad + u * stride, row = first + sub;
+            if (first >= rows) break;                    // (the whole warp)
+            const bool live = row < rows, is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
+            float a[8], b[8];
+            unpack8(ua[u], a);
+            unpack8(ub[u], b);
+            if (!is_v && i < rot) {
+                if (p.pairs) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a0 = a[2 * k], a1 = a[2 * k + 1], b0 = b[2 * k], b1 = b[2 * k + 1];
+                        a[2 * k] = fmaf(a0, cs[k].x, -a1 * cs[k].y);
+                        a[2 * k + 1] = fmaf(a1, cs[k].x, a0 * cs[k].y);
+                        b[2 * k] = fmaf(b0, cs[4 + k].x, -b1 * cs[4 + k].y);
+                        b[2 * k + 1] = fmaf(b1, cs[4 + k].x, b0 * cs[4 + k].y);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float a0 = a[k], b0 = b[k];
+                        a[k] = fmaf(a0, cs[k].x, -b0 * cs[k].y);
+                        b[k] = fmaf(b0, cs[k].x, a0 * cs[k].y);
+                    }
+                }
+            }
+            if (live && is_q) {
+                uint4* dst = reinterpret_cast<uint4*>(p.q_out + ((int64_t)tok * p.Hq + row) * 128);
+                dst[ca] = pack8(a);
+                dst[cb] = pack8(b);
+            }
+            if (first + 4 > p.Hq)                        // (the whole warp: the row's amax is taken by all of it)
+                store_kv_row<kKind>(p, i, ca, cb, is_v, is_v ? row - p.Hq - p.Hkv : row - p.Hq, slot, live && !is_q, a, b,
+                                    ua[u], ub[u]);
         }
-        if (!live) continue;
-        if (is_q) {
-            uint4* dst = reinterpret_cast<uint4*>(p.q_out + ((int64_t)tok * p.Hq + row) * 128);
-            dst[ca] = pack8(a);
-            dst[cb] = pack8(b);
-            continue;
+        load(quad + sub + kRopeBatch * stride);
+    }
+}
+
+// The write without rotation into an 8-bit cache: the K and V rows of all tokens in one run, kRowBatch
+// rows in flight per thread.
+__global__ void __launch_bounds__(256) cache_write_int8_kernel(const RopeWriteParams p) {
+    const int i = threadIdx.x & 7;
+    const int64_t group = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3), groups = (int64_t)gridDim.x * 32;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int rows = 2 * p.Hkv;
+    const int64_t total = (int64_t)p.num_tokens * rows;
+    uint4 ua[kRowBatch], ub[kRowBatch];
+    int64_t slot[kRowBatch];
+    int row[kRowBatch];
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+        const int64_t item = group + u * groups;
+        slot[u] = -1;
+        row[u] = 0;
+        ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
+        if (item < total) {
+            const int tok = (int)(item / rows);
+            row[u] = (int)(item - (int64_t)tok * rows);
+            slot[u] = __ldg(p.slot_mapping + tok);
+            const __half* src = row[u] < p.Hkv ? p.k_new + ((int64_t)tok * p.Hkv + row[u]) * 128
+                                               : p.v_new + ((int64_t)tok * p.Hkv + row[u] - p.Hkv) * 128;
+            ua[u] = ld_stream_16(reinterpret_cast<const uint4*>(src) + 2 * i);
+            ub[u] = ld_stream_16(reinterpret_cast<const uint4*>(src) + 2 * i + 1);
         }
-        const int64_t slot = __ldg(p.slot_mapping + tok);
-        if (slot < 0) continue;                          // padding token
-        const int h = is_v ? row - p.Hq - p.Hkv : row - p.Hq;
-        if (slot >= p.num_slots) {
-            if (i == 0 && h == 0) flag_error(PKV_DEVERR_SLOT);
-            continue;
-        }
-        const int64_t dst = (slot * p.Hkv + h) * 16;     // in chunks of 8 channels
-        void* cache = is_v ? p.v_cache : p.k_cache;
-        if constexpr (kKind == kCacheF16) {
-            reinterpret_cast<uint4*>(cache)[dst + ca] = is_v ? va : pack8(a);
-            reinterpret_cast<uint4*>(cache)[dst + cb] = is_v ? vb : pack8(b);
-        } else if constexpr (kKind == kCacheFp8) {
-            float s = is_v ? p.v_scale : p.k_scale;
-            if (p.k_scales) s = head_scale(is_v ? p.v_scales : p.k_scales, p.scales_per_head, h);
-            reinterpret_cast<uint2*>(cache)[dst + ca] = quantize8_e4m3_f32(a, s);
-            reinterpret_cast<uint2*>(cache)[dst + cb] = quantize8_e4m3_f32(b, s);
-        } else {
-            reinterpret_cast<uint2*>(cache)[dst + ca] = quantize8_int8(a, scale);
-            reinterpret_cast<uint2*>(cache)[dst + cb] = quantize8_int8(b, scale);
-            if (i == 0) p.kv_scales[((slot / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot % 16] = scale;
-        }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+        float a[8], b[8];
+        unpack8(ua[u], a);
+        unpack8(ub[u], b);
+        const bool is_v = row[u] >= p.Hkv;
+        store_kv_row<kCacheInt8>(p, i, 2 * i, 2 * i + 1, is_v, is_v ? row[u] - p.Hkv : row[u], slot[u], true, a, b, ua[u],
+                                 ub[u]);
     }
 }
 
@@ -256,9 +353,13 @@ struct CacheReadParams {
 
 // Eight 8-bit codes times their scale, in fp32, rounded once to f16.
 __device__ __forceinline__ uint4 dequantize8_int8(uint2 u, float s) {
+    uint32_t h[4];
+    codes_to_half2x2(u.x, h[0], h[1]);
+    codes_to_half2x2(u.y, h[2], h[3]);
     float f[8];
+    unpack8(make_uint4(h[0], h[1], h[2], h[3]), f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = (float)((int)(((k < 4 ? u.x : u.y) >> (8 * (k & 3))) & 0xff) - 128) * s;
+    for (int k = 0; k < 8; ++k) f[k] *= s;
     return pack8(f);
 }
 
@@ -273,44 +374,65 @@ __device__ __forceinline__ uint4 dequantize8_e4m3(uint2 u, float s) {
     return pack8(f);
 }
 
-// Eight threads a row, two 8-channel chunks each, as in the write.
+// Eight threads a row, two 8-channel chunks each; kRowBatch rows in flight per thread.
 template <int kKind>
 __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p) {
     const int i = threadIdx.x & 7;
-    const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 3) + (threadIdx.x >> 3);
+    const int64_t group = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3), groups = (int64_t)gridDim.x * 32;
     grid_dependency_wait();
     grid_dependents_launch();
     const int rows = 2 * p.Hkv;
-    if (item >= (int64_t)p.num_tokens * rows) return;
-    const int tok = (int)(item / rows), row = (int)(item - (int64_t)tok * rows);
-    const int64_t slot = __ldg(p.slot_mapping + tok);
-    if (slot < 0) return;
-    const bool is_v = row >= p.Hkv;
-    const int h = is_v ? row - p.Hkv : row;
-    if (slot >= p.num_slots) {
-        if (i == 0 && row == 0) flag_error(PKV_DEVERR_SLOT);
-        return;
+    const int64_t total = (int64_t)p.num_tokens * rows;
+    int64_t slot[kRowBatch];
+    int tok[kRowBatch], row[kRowBatch];
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+        const int64_t item = group + u * groups;
+        slot[u] = -1;
+        if (item < total) {
+            tok[u] = (int)(item / rows);
+            row[u] = (int)(item - (int64_t)tok[u] * rows);
+            slot[u] = __ldg(p.slot_mapping + tok[u]);
+            if (slot[u] >= p.num_slots) {
+                if (i == 0 && row[u] == 0) flag_error(PKV_DEVERR_SLOT);
+                slot[u] = -1;
+            }
+        }
     }
-    const int64_t src = (slot * p.Hkv + h) * 16;
-    const void* cache = is_v ? p.v_cache : p.k_cache;
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)tok * p.Hkv + h) * 128);
-    if constexpr (kKind == kCacheF16) {
-        const uint4* s = reinterpret_cast<const uint4*>(cache) + src;
-        const uint4 a = __ldg(s + i), b = __ldg(s + i + 8);
-        dst[i] = a;
-        dst[i + 8] = b;
-    } else {
-        // 16 codes of one chunk pair: chunks 2i and 2i + 1
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint2*>(cache) + src) + i);
-        const uint2 lo = make_uint2(u.x, u.y), hi = make_uint2(u.z, u.w);
-        if constexpr (kKind == kCacheFp8) {
-            const float s = is_v ? p.v_scale : p.k_scale;
-            dst[2 * i] = dequantize8_e4m3(lo, s);
-            dst[2 * i + 1] = dequantize8_e4m3(hi, s);
+    uint4 x[kRowBatch], y[kRowBatch];
+    float s[kRowBatch];
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+        if (slot[u] < 0) continue;
+        const bool is_v = row[u] >= p.Hkv;
+        const int h = is_v ? row[u] - p.Hkv : row[u];
+        const int64_t src = (slot[u] * p.Hkv + h) * 16;
+        const void* cache = is_v ? p.v_cache : p.k_cache;
+        if constexpr (kKind == kCacheF16) {
+            x[u] = ld_stream_16(reinterpret_cast<const uint4*>(cache) + src + 2 * i);
+            y[u] = ld_stream_16(reinterpret_cast<const uint4*>(cache) + src + 2 * i + 1);
         } else {
-            const float s = __ldg(p.kv_scales + ((slot / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot % 16);
-            dst[2 * i] = dequantize8_int8(lo, s);
-            dst[2 * i + 1] = dequantize8_int8(hi, s);
+            x[u] = ld_stream_16(reinterpret_cast<const uint4*>(reinterpret_cast<const uint2*>(cache) + src) + i);
+            if constexpr (kKind == kCacheFp8) s[u] = is_v ? p.v_scale : p.k_scale;
+            else s[u] = __ldg(p.kv_scales + ((slot[u] / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot[u] % 16);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+        if (slot[u] < 0) continue;
+        const bool is_v = row[u] >= p.Hkv;
+        const int h = is_v ? row[u] - p.Hkv : row[u];
+        uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)tok[u] * p.Hkv + h) * 128) + 2 * i;
+        const uint2 lo = make_uint2(x[u].x, x[u].y), hi = make_uint2(x[u].z, x[u].w);
+        if constexpr (kKind == kCacheF16) {
+            dst[0] = x[u];
+            dst[1] = y[u];
+        } else if constexpr (kKind == kCacheFp8) {
+            dst[0] = dequantize8_e4m3(lo, s[u]);
+            dst[1] = dequantize8_e4m3(hi, s[u]);
+        } else {
+            dst[0] = dequantize8_int8(lo, s[u]);
+            dst[1] = dequantize8_int8(hi, s[u]);
         }
     }
 }

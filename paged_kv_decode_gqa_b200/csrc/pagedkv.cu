@@ -934,22 +934,29 @@ pkv_status check_cache_rows(const void* k_cache, const void* v_cache, const floa
     return PKV_OK;
 }
 
-// Launches the write for a checked call. One block of up to 512 threads takes
-// whole tokens, eight threads to a head row: enough tokens for 256 threads.
+// Launches the rotating write for a checked call. A token's rows go to one warp when the tokens alone
+// give every SM 16 warps, and are shared out over more warps (down to four rows each) below that.
 pkv_status launch_rope_write(pkv::RopeWriteParams& prm, int32_t kv_dtype, cudaStream_t st) {
-    const int rows = prm.Hq + 2 * prm.Hkv;
-    prm.tokens_per_block = std::max(1, std::min(32, 32 / rows));
-    const int64_t want = (int64_t)prm.tokens_per_block * rows * 8;
-    const int threads = (int)std::min<int64_t>(512, (want + 31) / 32 * 32);
-    const unsigned blocks = (unsigned)((prm.num_tokens + prm.tokens_per_block - 1) / prm.tokens_per_block);
-    const size_t smem = (size_t)prm.tokens_per_block * prm.half * sizeof(float2);
-    cudaError_t e;
-    switch (kv_dtype) {
-        case PKV_KV_F16: e = launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheF16>, dim3(blocks), dim3(threads), smem, st, prm); break;
-        case PKV_KV_FP8_E4M3: e = launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheFp8>, dim3(blocks), dim3(threads), smem, st, prm); break;
-        default: e = launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheInt8>, dim3(blocks), dim3(threads), smem, st, prm);
-    }
+    const int sms = device_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const int quads = (prm.Hq + 2 * prm.Hkv + 3) / 4;
+    const int64_t want = ((int64_t)sms * 16 + prm.num_tokens - 1) / prm.num_tokens;
+    prm.splits = (int)std::min<int64_t>(quads, want);
+    const int64_t blocks = ((int64_t)prm.num_tokens * prm.splits + pkv::kRopeWarps - 1) / pkv::kRopeWarps;
+    const dim3 g((unsigned)blocks), t(32 * pkv::kRopeWarps);
+    const cudaError_t e =
+        kv_dtype == PKV_KV_F16        ? launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheF16>, g, t, 0, st, prm)
+        : kv_dtype == PKV_KV_FP8_E4M3 ? launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheFp8>, g, t, 0, st, prm)
+                                      : launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheInt8>, g, t, 0, st, prm);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// Blocks of the kernels that take all tokens' K and V rows in one run: 32 rows at a time, kRowBatch times;
+// 0 when there are too many.
+unsigned row_blocks(int64_t num_tokens, int64_t num_kv_heads) {
+    const int64_t per = 32 * pkv::kRowBatch;
+    const int64_t blocks = (num_tokens * 2 * num_kv_heads + per - 1) / per;
+    return blocks > INT32_MAX ? 0u : (unsigned)blocks;
 }
 
 pkv_status rope_write_impl(void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache,
@@ -1350,7 +1357,7 @@ pkv_status paged_kv_cache_write_int8(const void* k_new, const void* v_new, void*
                                           num_blocks, block_size, PKV_KV_INT8, 1.f, 1.f);
     if (v != PKV_OK || num_tokens == 0) return v;
     if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return PKV_ERR_INVALID_ARG;
-    pkv::RopeWriteParams prm{};                      // no q heads, nothing rotated
+    pkv::RopeWriteParams prm{};
     prm.k_new = static_cast<const __half*>(k_new);
     prm.v_new = static_cast<const __half*>(v_new);
     prm.k_cache = k_cache;
@@ -1360,8 +1367,10 @@ pkv_status paged_kv_cache_write_int8(const void* k_new, const void* v_new, void*
     prm.num_slots = (int64_t)num_blocks * block_size;
     prm.num_tokens = num_tokens;
     prm.Hkv = num_kv_heads;
-    prm.axes = 1;
-    return launch_rope_write(prm, PKV_KV_INT8, static_cast<cudaStream_t>(stream));
+    const unsigned blocks = row_blocks(num_tokens, num_kv_heads);
+    if (!blocks) return PKV_ERR_UNSUPPORTED;
+    return launch_pdl(pkv::cache_write_int8_kernel, dim3(blocks), dim3(256), 0, static_cast<cudaStream_t>(stream), prm) ==
+                   cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status paged_kv_rope_cache_write(void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache,
@@ -1410,10 +1419,10 @@ pkv_status paged_kv_cache_read(void* k_out, void* v_out, const void* k_cache, co
     prm.Hkv = num_kv_heads;
     prm.k_scale = k_scale;
     prm.v_scale = v_scale;
-    const int64_t blocks = ((int64_t)num_tokens * 2 * num_kv_heads + 31) / 32;   // 32 head rows a block
-    if (blocks > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    const unsigned blocks = row_blocks(num_tokens, num_kv_heads);
+    if (!blocks) return PKV_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 g((unsigned)blocks), t(256);
+    const dim3 g(blocks), t(256);
     const cudaError_t e =
         kv_dtype == PKV_KV_F16        ? launch_pdl(pkv::cache_read_kernel<pkv::kCacheF16>, g, t, 0, st, prm)
         : kv_dtype == PKV_KV_FP8_E4M3 ? launch_pdl(pkv::cache_read_kernel<pkv::kCacheFp8>, g, t, 0, st, prm)

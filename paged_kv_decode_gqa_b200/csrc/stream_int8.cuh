@@ -72,24 +72,6 @@ struct StreamInt8Shape {
     static size_t smem_bytes(int B) { return (size_t)kFixed + ((size_t)(B + 1) * 4 + 15) / 16 * 16; }
 };
 
-// Four codes (low byte first) to two f16x2 of their exact values: 0x6400 | code
-// is 1024 + code in f16, and 1152 is subtracted exactly.
-__device__ __forceinline__ uint32_t sub_1152(uint32_t h) {
-    const uint32_t bias = 0x64806480u;
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
-// bytes (0, 1) and (2, 3): consecutive channels of one token
-__device__ __forceinline__ void codes_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    lo = sub_1152(prmt(w, 0x64646464u, 0x5140u));
-    hi = sub_1152(prmt(w, 0x64646464u, 0x5342u));
-}
-// bytes (0, 2) and (1, 3): one channel of two tokens each
-__device__ __forceinline__ void codes_to_half2x2_cross(uint32_t w, uint32_t& even, uint32_t& odd) {
-    even = sub_1152(prmt(w, 0x64646464u, 0x5240u));
-    odd = sub_1152(prmt(w, 0x64646464u, 0x5341u));
-}
-
 __device__ __forceinline__ float fast_log2(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
