@@ -115,49 +115,49 @@ __device__ __forceinline__ uint2 quantize8_e4m3_f32(const float (&f)[8], float s
     return make_uint2(w[0], w[1]);
 }
 
-// Largest finite magnitude of eight values (0 when none is finite).
-__device__ __forceinline__ float finite_amax8(const float (&f)[8], float m) {
+// Largest finite magnitude of 16 values (0 when none is finite). fmaxf ignores NaN; infinities are rare
+// enough to be sorted out afterwards.
+__device__ __forceinline__ float finite_amax16(const float (&a)[8], const float (&b)[8]) {
+    float m = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float a = fabsf(f[k]);
-        m = a <= 3.402823466e38f ? fmaxf(m, a) : m;
+    for (int k = 0; k < 8; ++k) m = fmaxf(fmaxf(m, fabsf(a[k])), fabsf(b[k]));
+    if (m > 3.402823466e38f) {
+        m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            m = fabsf(a[k]) <= 3.402823466e38f ? fmaxf(m, fabsf(a[k])) : m;
+            m = fabsf(b[k]) <= 3.402823466e38f ? fmaxf(m, fabsf(b[k])) : m;
+        }
     }
     return m;
 }
 
 // Codes 128 + round(x / scale) of eight values: nearest even, infinities at
 // +-127, NaN at 0; x / scale is the fp32 quotient, correctly rounded.
-// x * (1 / scale) is within 3 x 2^-24 x 128 < 2^-15 of that quotient (three
-// roundings of a value of at most 127), so both round to the same integer
-// unless the product lies within 2^-14 of a tie; only then (two values in
-// 10000, and where x is not finite) is the division done.
+// x * inv, inv = 1 / scale, taken exactly by the multiply-add, is within 2^-16
+// of that quotient (two roundings of a value of at most 127), so both round to
+// the same integer unless the product lies within 2^-14 of a tie; only then
+// (one value in 8000, and where x is not finite) is the division done.
 __device__ __forceinline__ uint2 quantize8_int8(const float (&f)[8], float scale, float inv) {
-    uint32_t w[2];
+    constexpr float kMagic = 12583040.f;                     // 1.5 x 2^23 + 128: the low byte of x + kMagic is the code
+    uint32_t c[8];
+    float worst = 0.f;
+    bool finite = true;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t c[4];
-        bool safe = true;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float q = f[4 * h + k] * inv;
-            const float r = q + 12583040.f;                  // 1.5 x 2^23 + 128: the low byte is the code
-            c[k] = __float_as_uint(r);
-            safe = safe && fabsf(q - (r - 12583040.f)) < 0.5f - 6.103515625e-5f;
-        }
-        if (!safe) {
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const float x = k == 0 ? f[4 * h] : k == 1 ? f[4 * h + 1] : k == 2 ? f[4 * h + 2] : f[4 * h + 3];
-                const uint32_t v = (uint32_t)(min(127, max(-127, __float2int_rn(x / scale))) + 128);   // NaN: 0
-                if (k == 0) c[0] = v;
-                else if (k == 1) c[1] = v;
-                else if (k == 2) c[2] = v;
-                else c[3] = v;
-            }
-        }
-        w[h] = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+    for (int k = 0; k < 8; ++k) {
+        const float r = fmaf(f[k], inv, kMagic);
+        c[k] = __float_as_uint(r);
+        const float d = fabsf(fmaf(f[k], inv, kMagic - r));  // distance from the integer taken
+        worst = fmaxf(worst, d);
+        finite = finite && d < 1.f;                          // (false for NaN, which fmaxf would drop)
     }
-    return make_uint2(w[0], w[1]);
+    if (worst > 0.5f - 6.103515625e-5f || !finite) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            c[k] = (uint32_t)(min(127, max(-127, __float2int_rn(f[k] / scale))) + 128);   // NaN gives 0
+    }
+    return make_uint2(prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u),
+                      prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u));
 }
 
 // Position axis of frequency j.
@@ -173,16 +173,16 @@ __device__ __forceinline__ int rope_axis(const RopeWriteParams& p, int j) {
 
 constexpr int kRopeWarps = 4;       // warps of a block, each on its own
 constexpr int kRopeBatch = 3;       // rows in flight per thread of the rotating write
-constexpr int kRowBatch = 4;        // and of the plain write and the read
+constexpr int kRowBatch = 2;        // and of the plain write and the read
 
 // Stores one head row's eight-thread share (chunks ca, cb as fp32 a, b; as read: ua, ub) of K or V.
-template <int kKind>
+template <int kKind, bool kPlain = false>
 __device__ __forceinline__ void store_kv_row(const RopeWriteParams& p, int i, int ca, int cb, bool is_v, int h,
                                              int64_t slot, bool live, const float (&a)[8], const float (&b)[8],
                                              const uint4& ua, const uint4& ub) {
     float scale = 1.f;
     if constexpr (kKind == kCacheInt8) {             // amax of the row, over its eight threads
-        float m = finite_amax8(b, finite_amax8(a, 0.f));
+        float m = finite_amax16(a, b);
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         scale = fmaxf(m, kInt8MinAmax) / 127.f;
@@ -204,8 +204,13 @@ __device__ __forceinline__ void store_kv_row(const RopeWriteParams& p, int i, in
         reinterpret_cast<uint2*>(cache)[dst + cb] = quantize8_e4m3_f32(b, s);
     } else {
         const float inv = 1.f / scale;
-        reinterpret_cast<uint2*>(cache)[dst + ca] = quantize8_int8(a, scale, inv);
-        reinterpret_cast<uint2*>(cache)[dst + cb] = quantize8_int8(b, scale, inv);
+        const uint2 x = quantize8_int8(a, scale, inv), y = quantize8_int8(b, scale, inv);
+        if (kPlain) {                                // neighbouring chunks
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint2*>(cache) + dst + ca) = make_uint4(x.x, x.y, y.x, y.y);
+        } else {
+            reinterpret_cast<uint2*>(cache)[dst + ca] = x;
+            reinterpret_cast<uint2*>(cache)[dst + cb] = y;
+        }
         if (i == 0) p.kv_scales[((slot / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot % 16] = scale;
     }
 }
@@ -214,8 +219,10 @@ template <int kKind>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const RopeWriteParams p) {
     __shared__ float2 s_turn[kRopeWarps][64];            // (cos, sin) of the warp's token
     const int lane = threadIdx.x & 31, i = lane & 7, sub = lane >> 3;
-    const int64_t warp = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-    const int tok = (int)(warp / p.splits), split = (int)(warp - (int64_t)tok * p.splits);
+    const int warp = (int)blockIdx.x * kRopeWarps + (int)(threadIdx.x >> 5);
+    const int step = (int)(gridDim.x * kRopeWarps) / p.splits;       // tokens between a warp's turns
+    int tok = warp / p.splits;
+    const int split = warp - tok * p.splits;
     const int rows = p.Hq + 2 * p.Hkv;                   // q heads, k heads, v heads
     const int rot = p.half >> 3;                         // threads of a row that hold rotated pairs
     const int ca = i < rot ? i : 2 * i, cb = i < rot ? i + rot : 2 * i + 1;   // this thread's chunks
@@ -224,86 +231,114 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const
     grid_dependents_launch();
     if (kKind == kCacheFp8 && p.k_scales && blockIdx.x == 0)
         check_scales(p.k_scales, p.v_scales, p.scales_per_head ? p.Hkv : 1, threadIdx.x, blockDim.x);
-    if (tok >= p.num_tokens) return;
+    if (tok >= p.num_tokens || tok >= step) return;      // (warps left over by an uneven split)
 
-    // rows 4 (split + splits k) + sub, k = 0, 1, ...
+    // A token's rows of this warp: first + sub, first = 4 split, 4 split + stride, ..., in batches of
+    // kRopeBatch. Every row's registers are refilled as soon as it is done, with the row a batch ahead:
+    // of this token, or of the warp's next.
     const int stride = 4 * p.splits;
     uint4 ua[kRopeBatch], ub[kRopeBatch];
-    auto load = [&](int row0) {
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            const int row = row0 + u * stride;
-            if (row < rows) {
-                const __half* s = row < p.Hq ? p.q + ((int64_t)tok * p.Hq + row) * 128
-                                  : row < p.Hq + p.Hkv ? p.k_new + ((int64_t)tok * p.Hkv + (row - p.Hq)) * 128
-                                                       : p.v_new + ((int64_t)tok * p.Hkv + (row - p.Hq - p.Hkv)) * 128;
-                ua[u] = ld_once_16(reinterpret_cast<const uint4*>(s) + ca);
-                ub[u] = ld_once_16(reinterpret_cast<const uint4*>(s) + cb);
-            }
+    auto load = [&](int u, int t, int row) {
+        if (t < p.num_tokens && row < rows) {
+            const __half* s = row < p.Hq ? p.q + ((int64_t)t * p.Hq + row) * 128
+                              : row < p.Hq + p.Hkv ? p.k_new + ((int64_t)t * p.Hkv + (row - p.Hq)) * 128
+                                                   : p.v_new + ((int64_t)t * p.Hkv + (row - p.Hq - p.Hkv)) * 128;
+            ua[u] = ld_once_16(reinterpret_cast<const uint4*>(s) + ca);
+            ub[u] = ld_once_16(reinterpret_cast<const uint4*>(s) + cb);
         }
     };
-    load(4 * split + sub);
-    const int64_t slot = __ldg(p.slot_mapping + tok);
-    float2* turn = s_turn[threadIdx.x >> 5];
-    for (int j = lane; j < p.half; j += 32) {
-        const int64_t pos = __ldg(p.positions + (int64_t)rope_axis(p, j) * p.num_tokens + tok);
-        const double turns = (double)pos * (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
-        const float frac = (float)(turns - rint(turns));     // in [-1/2, 1/2]
-        sincospif(2.f * frac, &turn[j].y, &turn[j].x);
-    }
-    __syncwarp();
-    // pair k of this thread: channels (2k, 2k + 1) of chunk a, then of chunk b; or channel k of both chunks
-    float2 cs[8];
-    if (i < rot) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) cs[k] = turn[p.pairs ? (k < 4 ? 4 * ca + k : 4 * cb + k - 4) : 8 * i + k];
-    }
-    for (int quad = 4 * split; quad < rows; quad += kRopeBatch * stride) {
+    for (int u = 0; u < kRopeBatch; ++u) load(u, tok, 4 * split + u * stride + sub);
+    // this lane's frequencies, in turns per position, and their axes
+    double freq[2] = {0.0, 0.0};
+    const int64_t* where[2] = {p.positions, p.positions};
 #pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            const int first = quad + u * stride, row = first + sub;
-            if (first >= rows) break;                    // (the whole warp)
-            const bool live = row < rows, is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
-            float a[8], b[8];
-            unpack8(ua[u], a);
-            unpack8(ub[u], b);
-            if (!is_v && i < rot) {
-                if (p.pairs) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float a0 = a[2 * k], a1 = a[2 * k + 1], b0 = b[2 * k], b1 = b[2 * k + 1];
-                        a[2 * k] = fmaf(a0, cs[k].x, -a1 * cs[k].y);
-                        a[2 * k + 1] = fmaf(a1, cs[k].x, a0 * cs[k].y);
-                        b[2 * k] = fmaf(b0, cs[4 + k].x, -b1 * cs[4 + k].y);
-                        b[2 * k + 1] = fmaf(b1, cs[4 + k].x, b0 * cs[4 + k].y);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float a0 = a[k], b0 = b[k];
-                        a[k] = fmaf(a0, cs[k].x, -b0 * cs[k].y);
-                        b[k] = fmaf(b0, cs[k].x, a0 * cs[k].y);
-                    }
-                }
-            }
-            if (live && is_q) {
-                uint4* dst = reinterpret_cast<uint4*>(p.q_out + ((int64_t)tok * p.Hq + row) * 128);
-                dst[ca] = pack8(a);
-                dst[cb] = pack8(b);
-            }
-            if (first + 4 > p.Hq)                        // (the whole warp: the row's amax is taken by all of it)
-                store_kv_row<kKind>(p, i, ca, cb, is_v, is_v ? row - p.Hq - p.Hkv : row - p.Hq, slot, live && !is_q, a, b,
-                                    ua[u], ub[u]);
+    for (int e = 0; e < 2; ++e) {
+        const int j = lane + 32 * e;
+        if (j < p.half) {
+            freq[e] = (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
+            where[e] += (int64_t)rope_axis(p, j) * p.num_tokens;
         }
-        load(quad + sub + kRopeBatch * stride);
+    }
+    int64_t pos[2] = {__ldg(where[0] + tok), __ldg(where[1] + tok)};
+    int64_t slot = __ldg(p.slot_mapping + tok);
+    float2* turn = s_turn[threadIdx.x >> 5];
+    while (tok < p.num_tokens) {
+        const int next = tok + step < p.num_tokens && tok + step >= 0 ? tok + step : p.num_tokens;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int j = lane + 32 * e;
+            if (j < p.half) {
+                const double turns = (double)pos[e] * freq[e];
+                const float frac = (float)(turns - rint(turns));     // in [-1/2, 1/2]
+                sincospif(2.f * frac, &turn[j].y, &turn[j].x);
+            }
+        }
+        __syncwarp();
+        // pair k of this thread: channels (2k, 2k + 1) of chunk a, then of chunk b; or channel k of both
+        float2 cs[8];
+        if (i < rot) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) cs[k] = turn[p.pairs ? (k < 4 ? 4 * ca + k : 4 * cb + k - 4) : 8 * i + k];
+        }
+        __syncwarp();                                    // before the next token's angles
+        const int64_t this_slot = slot;
+        if (next < p.num_tokens) {
+            pos[0] = __ldg(where[0] + next);
+            pos[1] = __ldg(where[1] + next);
+            slot = __ldg(p.slot_mapping + next);
+        }
+        for (int first0 = 4 * split; first0 < rows; first0 += kRopeBatch * stride) {
+            const bool more = first0 + kRopeBatch * stride < rows;       // batches left of this token
+#pragma unroll
+            for (int u = 0; u < kRopeBatch; ++u) {
+                const int first = first0 + u * stride, row = first + sub;
+                if (first < rows) {                      // (the whole warp)
+                    const bool live = row < rows, is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
+                    float a[8], b[8];
+                    unpack8(ua[u], a);
+                    unpack8(ub[u], b);
+                    if (!is_v && i < rot) {
+                        if (p.pairs) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float a0 = a[2 * k], a1 = a[2 * k + 1], b0 = b[2 * k], b1 = b[2 * k + 1];
+                                a[2 * k] = fmaf(a0, cs[k].x, -a1 * cs[k].y);
+                                a[2 * k + 1] = fmaf(a1, cs[k].x, a0 * cs[k].y);
+                                b[2 * k] = fmaf(b0, cs[4 + k].x, -b1 * cs[4 + k].y);
+                                b[2 * k + 1] = fmaf(b1, cs[4 + k].x, b0 * cs[4 + k].y);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float a0 = a[k], b0 = b[k];
+                                a[k] = fmaf(a0, cs[k].x, -b0 * cs[k].y);
+                                b[k] = fmaf(b0, cs[k].x, a0 * cs[k].y);
+                            }
+                        }
+                    }
+                    if (live && is_q) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.q_out + ((int64_t)tok * p.Hq + row) * 128);
+                        dst[ca] = pack8(a);
+                        dst[cb] = pack8(b);
+                    }
+                    if (first + 4 > p.Hq)                // (the whole warp: it takes the row's amax together)
+                        store_kv_row<kKind>(p, i, ca, cb, is_v, is_v ? row - p.Hq - p.Hkv : row - p.Hq, this_slot,
+                                            live && !is_q, a, b, ua[u], ub[u]);
+                }
+                if (more) load(u, tok, row + kRopeBatch * stride);
+                else load(u, next, 4 * split + u * stride + sub);
+            }
+        }
+        tok = next;
     }
 }
 
-// The write without rotation into an 8-bit cache: the K and V rows of all tokens in one run, kRowBatch
-// rows in flight per thread.
+// The write without rotation into an 8-bit cache: the K and V rows of all tokens in one run; a thread
+// keeps kRowBatch rows in flight and refills each as soon as it is done.
 __global__ void __launch_bounds__(256) cache_write_int8_kernel(const RopeWriteParams p) {
     const int i = threadIdx.x & 7;
-    const int64_t group = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3), groups = (int64_t)gridDim.x * 32;
+    const int64_t groups = (int64_t)gridDim.x * 32;
     grid_dependency_wait();
     grid_dependents_launch();
     const int rows = 2 * p.Hkv;
@@ -311,30 +346,37 @@ __global__ void __launch_bounds__(256) cache_write_int8_kernel(const RopeWritePa
     uint4 ua[kRowBatch], ub[kRowBatch];
     int64_t slot[kRowBatch];
     int row[kRowBatch];
-#pragma unroll
-    for (int u = 0; u < kRowBatch; ++u) {
-        const int64_t item = group + u * groups;
+    auto load = [&](int u, int64_t item) {
         slot[u] = -1;
         row[u] = 0;
-        ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
         if (item < total) {
             const int tok = (int)(item / rows);
             row[u] = (int)(item - (int64_t)tok * rows);
-            slot[u] = __ldg(p.slot_mapping + tok);
             const __half* src = row[u] < p.Hkv ? p.k_new + ((int64_t)tok * p.Hkv + row[u]) * 128
                                                : p.v_new + ((int64_t)tok * p.Hkv + row[u] - p.Hkv) * 128;
             ua[u] = ld_stream_16(reinterpret_cast<const uint4*>(src) + 2 * i);
             ub[u] = ld_stream_16(reinterpret_cast<const uint4*>(src) + 2 * i + 1);
+            slot[u] = __ldg(p.slot_mapping + tok);
         }
-    }
+    };
+    int64_t item = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
 #pragma unroll
     for (int u = 0; u < kRowBatch; ++u) {
-        float a[8], b[8];
-        unpack8(ua[u], a);
-        unpack8(ub[u], b);
-        const bool is_v = row[u] >= p.Hkv;
-        store_kv_row<kCacheInt8>(p, i, 2 * i, 2 * i + 1, is_v, is_v ? row[u] - p.Hkv : row[u], slot[u], true, a, b, ua[u],
-                                 ub[u]);
+        ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
+        load(u, item + u * groups);
+    }
+    const int64_t warp_first = (int64_t)blockIdx.x * 32 + ((threadIdx.x >> 5) << 2);   // uniform in the warp
+    for (int64_t base = warp_first; base < total; base += kRowBatch * groups, item += kRowBatch * groups) {
+#pragma unroll
+        for (int u = 0; u < kRowBatch; ++u) {
+            float a[8], b[8];
+            unpack8(ua[u], a);
+            unpack8(ub[u], b);
+            const bool is_v = row[u] >= p.Hkv;
+            store_kv_row<kCacheInt8, true>(p, i, 2 * i, 2 * i + 1, is_v, is_v ? row[u] - p.Hkv : row[u], slot[u], true, a,
+                                           b, ua[u], ub[u]);
+            load(u, item + (kRowBatch + u) * groups);
+        }
     }
 }
 
@@ -374,65 +416,74 @@ __device__ __forceinline__ uint4 dequantize8_e4m3(uint2 u, float s) {
     return pack8(f);
 }
 
-// Eight threads a row, two 8-channel chunks each; kRowBatch rows in flight per thread.
+// Eight threads a row, two 8-channel chunks each; kRowBatch rows in flight per thread, each refilled as
+// soon as it is done, and their slots one batch further ahead.
 template <int kKind>
 __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p) {
     const int i = threadIdx.x & 7;
-    const int64_t group = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3), groups = (int64_t)gridDim.x * 32;
+    const int64_t groups = (int64_t)gridDim.x * 32;
     grid_dependency_wait();
     grid_dependents_launch();
     const int rows = 2 * p.Hkv;
     const int64_t total = (int64_t)p.num_tokens * rows;
-    int64_t slot[kRowBatch];
-    int tok[kRowBatch], row[kRowBatch];
-#pragma unroll
-    for (int u = 0; u < kRowBatch; ++u) {
-        const int64_t item = group + u * groups;
-        slot[u] = -1;
-        if (item < total) {
-            tok[u] = (int)(item / rows);
-            row[u] = (int)(item - (int64_t)tok[u] * rows);
-            slot[u] = __ldg(p.slot_mapping + tok[u]);
-            if (slot[u] >= p.num_slots) {
-                if (i == 0 && row[u] == 0) flag_error(PKV_DEVERR_SLOT);
-                slot[u] = -1;
-            }
-        }
-    }
+    auto slot_of = [&](int64_t item) -> int64_t { return item < total ? __ldg(p.slot_mapping + (int)(item / rows)) : -1; };
+    int64_t item = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    int64_t ahead[kRowBatch];                            // slots of the next batch
     uint4 x[kRowBatch], y[kRowBatch];
     float s[kRowBatch];
-#pragma unroll
-    for (int u = 0; u < kRowBatch; ++u) {
-        if (slot[u] < 0) continue;
-        const bool is_v = row[u] >= p.Hkv;
-        const int h = is_v ? row[u] - p.Hkv : row[u];
-        const int64_t src = (slot[u] * p.Hkv + h) * 16;
-        const void* cache = is_v ? p.v_cache : p.k_cache;
-        if constexpr (kKind == kCacheF16) {
-            x[u] = ld_stream_16(reinterpret_cast<const uint4*>(cache) + src + 2 * i);
-            y[u] = ld_stream_16(reinterpret_cast<const uint4*>(cache) + src + 2 * i + 1);
-        } else {
-            x[u] = ld_stream_16(reinterpret_cast<const uint4*>(reinterpret_cast<const uint2*>(cache) + src) + i);
-            if constexpr (kKind == kCacheFp8) s[u] = is_v ? p.v_scale : p.k_scale;
-            else s[u] = __ldg(p.kv_scales + ((slot[u] / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot[u] % 16);
+    bool live[kRowBatch];
+    auto load = [&](int u, int64_t it, int64_t slot) {
+        live[u] = slot >= 0 && slot < p.num_slots;
+        if (it < total && slot >= 0) {
+            const int row = (int)(it % rows);
+            if (!live[u]) {
+                if (i == 0 && row == 0) flag_error(PKV_DEVERR_SLOT);
+                return;
+            }
+            const bool is_v = row >= p.Hkv;
+            const int h = is_v ? row - p.Hkv : row;
+            const int64_t src = (slot * p.Hkv + h) * 16;
+            const void* cache = is_v ? p.v_cache : p.k_cache;
+            if constexpr (kKind == kCacheF16) {
+                x[u] = ld_stream_16(reinterpret_cast<const uint4*>(cache) + src + 2 * i);
+                y[u] = ld_stream_16(reinterpret_cast<const uint4*>(cache) + src + 2 * i + 1);
+            } else {
+                x[u] = ld_stream_16(reinterpret_cast<const uint4*>(reinterpret_cast<const uint2*>(cache) + src) + i);
+                if constexpr (kKind == kCacheFp8) s[u] = is_v ? p.v_scale : p.k_scale;
+                else s[u] = __ldg(p.kv_scales + ((slot / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot % 16);
+            }
         }
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) ahead[u] = slot_of(item + u * groups);
 #pragma unroll
     for (int u = 0; u < kRowBatch; ++u) {
-        if (slot[u] < 0) continue;
-        const bool is_v = row[u] >= p.Hkv;
-        const int h = is_v ? row[u] - p.Hkv : row[u];
-        uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)tok[u] * p.Hkv + h) * 128) + 2 * i;
-        const uint2 lo = make_uint2(x[u].x, x[u].y), hi = make_uint2(x[u].z, x[u].w);
-        if constexpr (kKind == kCacheF16) {
-            dst[0] = x[u];
-            dst[1] = y[u];
-        } else if constexpr (kKind == kCacheFp8) {
-            dst[0] = dequantize8_e4m3(lo, s[u]);
-            dst[1] = dequantize8_e4m3(hi, s[u]);
-        } else {
-            dst[0] = dequantize8_int8(lo, s[u]);
-            dst[1] = dequantize8_int8(hi, s[u]);
+        load(u, item + u * groups, ahead[u]);
+        ahead[u] = slot_of(item + (kRowBatch + u) * groups);
+    }
+    for (; item < total; item += kRowBatch * groups) {
+#pragma unroll
+        for (int u = 0; u < kRowBatch; ++u) {
+            const int64_t it = item + u * groups;
+            if (live[u]) {
+                const int tok = (int)(it / rows), row = (int)(it - (int64_t)tok * rows);
+                const bool is_v = row >= p.Hkv;
+                const int h = is_v ? row - p.Hkv : row;
+                uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)tok * p.Hkv + h) * 128) + 2 * i;
+                const uint2 lo = make_uint2(x[u].x, x[u].y), hi = make_uint2(x[u].z, x[u].w);
+                if constexpr (kKind == kCacheF16) {
+                    dst[0] = x[u];
+                    dst[1] = y[u];
+                } else if constexpr (kKind == kCacheFp8) {
+                    dst[0] = dequantize8_e4m3(lo, s[u]);
+                    dst[1] = dequantize8_e4m3(hi, s[u]);
+                } else {
+                    dst[0] = dequantize8_int8(lo, s[u]);
+                    dst[1] = dequantize8_int8(hi, s[u]);
+                }
+            }
+            load(u, it + kRowBatch * groups, ahead[u]);
+            ahead[u] = slot_of(it + 2 * kRowBatch * groups);
         }
     }
 }

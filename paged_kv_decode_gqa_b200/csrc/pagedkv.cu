@@ -934,29 +934,46 @@ pkv_status check_cache_rows(const void* k_cache, const void* v_cache, const floa
     return PKV_OK;
 }
 
-// Launches the rotating write for a checked call. A token's rows go to one warp when the tokens alone
-// give every SM 16 warps, and are shared out over more warps (down to four rows each) below that.
-pkv_status launch_rope_write(pkv::RopeWriteParams& prm, int32_t kv_dtype, cudaStream_t st) {
-    const int sms = device_sms();
-    if (sms <= 0) return PKV_ERR_CUDA;
-    const int quads = (prm.Hq + 2 * prm.Hkv + 3) / 4;
-    const int64_t want = ((int64_t)sms * 16 + prm.num_tokens - 1) / prm.num_tokens;
-    prm.splits = (int)std::min<int64_t>(quads, want);
-    const int64_t blocks = ((int64_t)prm.num_tokens * prm.splits + pkv::kRopeWarps - 1) / pkv::kRopeWarps;
-    const dim3 g((unsigned)blocks), t(32 * pkv::kRopeWarps);
-    const cudaError_t e =
-        kv_dtype == PKV_KV_F16        ? launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheF16>, g, t, 0, st, prm)
-        : kv_dtype == PKV_KV_FP8_E4M3 ? launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheFp8>, g, t, 0, st, prm)
-                                      : launch_pdl(pkv::rope_cache_write_kernel<pkv::kCacheInt8>, g, t, 0, st, prm);
-    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+// Blocks of `threads` that fit on the device at once (0 on error), asked once per kernel and device.
+template <typename Kernel>
+int resident_blocks(Kernel kernel, int threads, int (&known)[64]) {
+    int dev = 0, per_sm = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int n = __atomic_load_n(&known[dev & 63], __ATOMIC_RELAXED);
+    if (n > 0) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess) return 0;
+    sms = device_sms();
+    n = per_sm * sms;
+    __atomic_store_n(&known[dev & 63], n, __ATOMIC_RELAXED);
+    return n;
 }
 
-// Blocks of the kernels that take all tokens' K and V rows in one run: 32 rows at a time, kRowBatch times;
-// 0 when there are too many.
-unsigned row_blocks(int64_t num_tokens, int64_t num_kv_heads) {
-    const int64_t per = 32 * pkv::kRowBatch;
-    const int64_t blocks = (num_tokens * 2 * num_kv_heads + per - 1) / per;
-    return blocks > INT32_MAX ? 0u : (unsigned)blocks;
+// Launches the rotating write for a checked call: as many blocks as fit, whose warps go on from token to
+// token; a token's rows are shared out over several warps (down to four rows each) when there are too few
+// tokens to give every SM 16 warps.
+template <int kKind>
+pkv_status launch_rope_write(pkv::RopeWriteParams& prm, cudaStream_t st) {
+    auto kernel = pkv::rope_cache_write_kernel<kKind>;
+    static int known[64];
+    const int fit = resident_blocks(kernel, 32 * pkv::kRopeWarps, known), sms = device_sms();
+    if (fit <= 0 || sms <= 0) return PKV_ERR_CUDA;
+    const int quads = (prm.Hq + 2 * prm.Hkv + 3) / 4;
+    const int64_t want = ((int64_t)sms * 16 + prm.num_tokens - 1) / prm.num_tokens;
+    prm.splits = (int)std::min<int64_t>(std::min<int64_t>(quads, want), (int64_t)fit * pkv::kRopeWarps);
+    const int64_t blocks = ((int64_t)prm.num_tokens * prm.splits + pkv::kRopeWarps - 1) / pkv::kRopeWarps;
+    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(blocks, fit)), dim3(32 * pkv::kRopeWarps), 0, st, prm) ==
+                   cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// Launches a kernel that takes all tokens' K and V rows in one run, 32 at a time to a block, on as many
+// blocks as there are rows for and as fit.
+template <typename Kernel, typename Params>
+pkv_status launch_rows(Kernel kernel, const Params& prm, int (&known)[64], cudaStream_t st) {
+    const int fit = resident_blocks(kernel, 256, known);
+    if (fit <= 0) return PKV_ERR_CUDA;
+    const int64_t blocks = ((int64_t)prm.num_tokens * 2 * prm.Hkv + 31) / 32;
+    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(blocks, fit)), dim3(256), 0, st, prm) == cudaSuccess
+               ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status rope_write_impl(void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache,
@@ -1018,7 +1035,10 @@ pkv_status rope_write_impl(void* q_out, const void* q, const void* k_new, const 
     prm.k_scales = ds.k;
     prm.v_scales = ds.v;
     prm.scales_per_head = ds.per_head;
-    return launch_rope_write(prm, kv_dtype, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return kv_dtype == PKV_KV_F16        ? launch_rope_write<pkv::kCacheF16>(prm, st)
+           : kv_dtype == PKV_KV_FP8_E4M3 ? launch_rope_write<pkv::kCacheFp8>(prm, st)
+                                         : launch_rope_write<pkv::kCacheInt8>(prm, st);
 }
 
 }  // namespace
@@ -1367,10 +1387,8 @@ pkv_status paged_kv_cache_write_int8(const void* k_new, const void* v_new, void*
     prm.num_slots = (int64_t)num_blocks * block_size;
     prm.num_tokens = num_tokens;
     prm.Hkv = num_kv_heads;
-    const unsigned blocks = row_blocks(num_tokens, num_kv_heads);
-    if (!blocks) return PKV_ERR_UNSUPPORTED;
-    return launch_pdl(pkv::cache_write_int8_kernel, dim3(blocks), dim3(256), 0, static_cast<cudaStream_t>(stream), prm) ==
-                   cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    static int known[64];
+    return launch_rows(pkv::cache_write_int8_kernel, prm, known, static_cast<cudaStream_t>(stream));
 }
 
 pkv_status paged_kv_rope_cache_write(void* q_out, const void* q, const void* k_new, const void* v_new, void* k_cache,
@@ -1419,15 +1437,11 @@ pkv_status paged_kv_cache_read(void* k_out, void* v_out, const void* k_cache, co
     prm.Hkv = num_kv_heads;
     prm.k_scale = k_scale;
     prm.v_scale = v_scale;
-    const unsigned blocks = row_blocks(num_tokens, num_kv_heads);
-    if (!blocks) return PKV_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 g(blocks), t(256);
-    const cudaError_t e =
-        kv_dtype == PKV_KV_F16        ? launch_pdl(pkv::cache_read_kernel<pkv::kCacheF16>, g, t, 0, st, prm)
-        : kv_dtype == PKV_KV_FP8_E4M3 ? launch_pdl(pkv::cache_read_kernel<pkv::kCacheFp8>, g, t, 0, st, prm)
-                                      : launch_pdl(pkv::cache_read_kernel<pkv::kCacheInt8>, g, t, 0, st, prm);
-    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    static int known[3][64];
+    return kv_dtype == PKV_KV_F16        ? launch_rows(pkv::cache_read_kernel<pkv::kCacheF16>, prm, known[0], st)
+           : kv_dtype == PKV_KV_FP8_E4M3 ? launch_rows(pkv::cache_read_kernel<pkv::kCacheFp8>, prm, known[1], st)
+                                         : launch_rows(pkv::cache_read_kernel<pkv::kCacheInt8>, prm, known[2], st);
 }
 
 size_t paged_gqa_decode_workspace_size_int8(void) {
