@@ -334,39 +334,55 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const
     }
 }
 
+// A walk over the K and V rows of all tokens (row < 2 Hkv of token tok), in steps of `items` rows:
+// advanced by addition, because a division per row would cost as much as quantising it.
+struct RowWalk {
+    int tok, row, dtok, drow, rows;
+    __device__ __forceinline__ RowWalk(int64_t first, int64_t items, int rows_) : rows(rows_) {
+        tok = (int)(first / rows);
+        row = (int)(first - (int64_t)tok * rows);
+        dtok = (int)(items / rows);
+        drow = (int)(items - (int64_t)dtok * rows);
+    }
+    __device__ __forceinline__ void next() {
+        row += drow;
+        const int carry = row >= rows ? 1 : 0;
+        row -= carry ? rows : 0;
+        tok = min(tok + dtok + carry, INT32_MAX / 2);    // (stays past the last token)
+    }
+};
+
 // The write without rotation into an 8-bit cache: the K and V rows of all tokens in one run; a thread
 // keeps kRowBatch rows in flight and refills each as soon as it is done.
-__global__ void __launch_bounds__(256) cache_write_int8_kernel(const RopeWriteParams p) {
+__global__ void __launch_bounds__(256, 4) cache_write_int8_kernel(const RopeWriteParams p) {
     const int i = threadIdx.x & 7;
     const int64_t groups = (int64_t)gridDim.x * 32;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int rows = 2 * p.Hkv;
-    const int64_t total = (int64_t)p.num_tokens * rows;
+    RowWalk walk((int64_t)blockIdx.x * 32 + (threadIdx.x >> 3), groups, 2 * p.Hkv);
+    // the warp's first row decides when it ends, so that all of it reaches the row maxima
+    RowWalk lead((int64_t)blockIdx.x * 32 + ((threadIdx.x >> 5) << 2), groups, 2 * p.Hkv);
     uint4 ua[kRowBatch], ub[kRowBatch];
     int64_t slot[kRowBatch];
     int row[kRowBatch];
-    auto load = [&](int u, int64_t item) {
+    auto load = [&](int u) {
         slot[u] = -1;
-        row[u] = 0;
-        if (item < total) {
-            const int tok = (int)(item / rows);
-            row[u] = (int)(item - (int64_t)tok * rows);
-            const __half* src = row[u] < p.Hkv ? p.k_new + ((int64_t)tok * p.Hkv + row[u]) * 128
-                                               : p.v_new + ((int64_t)tok * p.Hkv + row[u] - p.Hkv) * 128;
+        row[u] = walk.row;
+        if (walk.tok < p.num_tokens) {
+            const __half* src = walk.row < p.Hkv ? p.k_new + ((int64_t)walk.tok * p.Hkv + walk.row) * 128
+                                                 : p.v_new + ((int64_t)walk.tok * p.Hkv + walk.row - p.Hkv) * 128;
             ua[u] = ld_stream_16(reinterpret_cast<const uint4*>(src) + 2 * i);
             ub[u] = ld_stream_16(reinterpret_cast<const uint4*>(src) + 2 * i + 1);
-            slot[u] = __ldg(p.slot_mapping + tok);
+            slot[u] = __ldg(p.slot_mapping + walk.tok);
         }
+        walk.next();
     };
-    int64_t item = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
 #pragma unroll
     for (int u = 0; u < kRowBatch; ++u) {
         ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
-        load(u, item + u * groups);
+        load(u);
     }
-    const int64_t warp_first = (int64_t)blockIdx.x * 32 + ((threadIdx.x >> 5) << 2);   // uniform in the warp
-    for (int64_t base = warp_first; base < total; base += kRowBatch * groups, item += kRowBatch * groups) {
+    while (lead.tok < p.num_tokens) {
 #pragma unroll
         for (int u = 0; u < kRowBatch; ++u) {
             float a[8], b[8];
@@ -375,7 +391,8 @@ __global__ void __launch_bounds__(256) cache_write_int8_kernel(const RopeWritePa
             const bool is_v = row[u] >= p.Hkv;
             store_kv_row<kCacheInt8, true>(p, i, 2 * i, 2 * i + 1, is_v, is_v ? row[u] - p.Hkv : row[u], slot[u], true, a,
                                            b, ua[u], ub[u]);
-            load(u, item + (kRowBatch + u) * groups);
+            load(u);
+            lead.next();
         }
     }
 }
@@ -424,24 +441,22 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
     const int64_t groups = (int64_t)gridDim.x * 32;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int rows = 2 * p.Hkv;
-    const int64_t total = (int64_t)p.num_tokens * rows;
-    auto slot_of = [&](int64_t item) -> int64_t { return item < total ? __ldg(p.slot_mapping + (int)(item / rows)) : -1; };
-    int64_t item = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
-    int64_t ahead[kRowBatch];                            // slots of the next batch
+    const int64_t first = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    RowWalk out(first, groups, 2 * p.Hkv), in = out, look = out;     // rows stored, loaded, looked up
+    int64_t ahead[kRowBatch];                            // slots looked up
     uint4 x[kRowBatch], y[kRowBatch];
     float s[kRowBatch];
     bool live[kRowBatch];
-    auto load = [&](int u, int64_t it, int64_t slot) {
+    auto look_up = [&](int u) {
+        ahead[u] = look.tok < p.num_tokens ? __ldg(p.slot_mapping + look.tok) : -1;
+        look.next();
+    };
+    auto load = [&](int u) {
+        const int64_t slot = ahead[u];
         live[u] = slot >= 0 && slot < p.num_slots;
-        if (it < total && slot >= 0) {
-            const int row = (int)(it % rows);
-            if (!live[u]) {
-                if (i == 0 && row == 0) flag_error(PKV_DEVERR_SLOT);
-                return;
-            }
-            const bool is_v = row >= p.Hkv;
-            const int h = is_v ? row - p.Hkv : row;
+        if (live[u]) {
+            const bool is_v = in.row >= p.Hkv;
+            const int h = is_v ? in.row - p.Hkv : in.row;
             const int64_t src = (slot * p.Hkv + h) * 16;
             const void* cache = is_v ? p.v_cache : p.k_cache;
             if constexpr (kKind == kCacheF16) {
@@ -452,24 +467,25 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
                 if constexpr (kKind == kCacheFp8) s[u] = is_v ? p.v_scale : p.k_scale;
                 else s[u] = __ldg(p.kv_scales + ((slot / 16 * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * 16 + slot % 16);
             }
+        } else if (slot >= 0 && i == 0 && in.row == 0) {
+            flag_error(PKV_DEVERR_SLOT);
         }
+        in.next();
     };
 #pragma unroll
-    for (int u = 0; u < kRowBatch; ++u) ahead[u] = slot_of(item + u * groups);
+    for (int u = 0; u < kRowBatch; ++u) look_up(u);
 #pragma unroll
     for (int u = 0; u < kRowBatch; ++u) {
-        load(u, item + u * groups, ahead[u]);
-        ahead[u] = slot_of(item + (kRowBatch + u) * groups);
+        load(u);
+        look_up(u);
     }
-    for (; item < total; item += kRowBatch * groups) {
+    while (out.tok < p.num_tokens) {
 #pragma unroll
         for (int u = 0; u < kRowBatch; ++u) {
-            const int64_t it = item + u * groups;
             if (live[u]) {
-                const int tok = (int)(it / rows), row = (int)(it - (int64_t)tok * rows);
-                const bool is_v = row >= p.Hkv;
-                const int h = is_v ? row - p.Hkv : row;
-                uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)tok * p.Hkv + h) * 128) + 2 * i;
+                const bool is_v = out.row >= p.Hkv;
+                const int h = is_v ? out.row - p.Hkv : out.row;
+                uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)out.tok * p.Hkv + h) * 128) + 2 * i;
                 const uint2 lo = make_uint2(x[u].x, x[u].y), hi = make_uint2(x[u].z, x[u].w);
                 if constexpr (kKind == kCacheF16) {
                     dst[0] = x[u];
@@ -482,8 +498,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
                     dst[1] = dequantize8_int8(hi, s[u]);
                 }
             }
-            load(u, it + kRowBatch * groups, ahead[u]);
-            ahead[u] = slot_of(it + 2 * kRowBatch * groups);
+            out.next();
+            load(u);
+            look_up(u);
         }
     }
 }
