@@ -456,9 +456,24 @@ def _take(name, t, dtype, shape, device):
     return t.data_ptr()
 
 
-def _raw_stream(stream, torch, device):
+_torch = _current_device = _current_stream = None
+
+
+def _runtime():
+    """torch, looked up once, and the two queries each call makes (the raw forms: the public ones build
+    a Stream object and re-check the initialisation, over a microsecond a call)."""
+    global _torch, _current_device, _current_stream
+    import torch
+    load_library()
+    _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    torch.cuda.init()
+    _torch = torch
+    return torch
+
+
+def _raw_stream(stream, device):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -486,30 +501,30 @@ def _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device):
 def paged_kv_cache_write_int8(k_new, v_new, k_cache, v_cache, kv_scales, slot_mapping, *, stream=None) -> None:
     """paged_kv_cache_write into an 8-bit cache: codes 128 + round(x / s) (uint8) and, in
     kv_scales [NB, Hkv, 2, 16] float32, s = max(max|x|, 2**-24) / 127 of every token and KV head."""
-    import torch
-    device = torch.cuda.current_device()
+    torch = _torch or _runtime()
+    device = _current_device()
     kc, vc, sc, NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales, torch, device)
     T = slot_mapping.numel()
     rows = (T, Hkv, D)
-    _check((_lib or load_library()).paged_kv_cache_write_int8(
+    _check(_lib.paged_kv_cache_write_int8(
         _take("k_new", k_new, torch.float16, rows, device), _take("v_new", v_new, torch.float16, rows, device),
         kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
-        _raw_stream(stream, torch, device)), "paged_kv_cache_write_int8")
+        _raw_stream(stream, device)), "paged_kv_cache_write_int8")
 
 
 def paged_kv_cache_read(k_out, v_out, k_cache, v_cache, slot_mapping, *, kv_dtype="f16", kv_scales=None,
                         k_scale=1.0, v_scale=1.0, stream=None) -> None:
     """k_out[i], v_out[i] ([T, Hkv, D] float16) = the cached values of slot slot_mapping[i], for an
     "f16", "fp8" or "int8" cache. Rows of negative slots are left as they were."""
-    import torch
-    device = torch.cuda.current_device()
+    torch = _torch or _runtime()
+    device = _current_device()
     kc, vc, sc, NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device)
     T = slot_mapping.numel()
     rows = (T, Hkv, D)
-    _check((_lib or load_library()).paged_kv_cache_read(
+    _check(_lib.paged_kv_cache_read(
         _take("k_out", k_out, torch.float16, rows, device), _take("v_out", v_out, torch.float16, rows, device),
         kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
-        code, k_scale, v_scale, _raw_stream(stream, torch, device)), "paged_kv_cache_read")
+        code, k_scale, v_scale, _raw_stream(stream, device)), "paged_kv_cache_read")
 
 
 def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq, *,
@@ -524,8 +539,8 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
     (j, j + rotary_dim / 2). For an "fp8" cache k_scale and v_scale are numbers, or float32 CUDA
     tensors of 1 or Hkv elements.
     """
-    import torch
-    device = torch.cuda.current_device()
+    torch = _torch or _runtime()
+    device = _current_device()
     kc, vc, sc, NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device)
     T = slot_mapping.numel()
     where = positions.shape
@@ -541,7 +556,7 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
     Hq = q.shape[1]
     rows, kv_rows = (T, Hq, D), (T, Hkv, D)
     flags = (PKV_ROPE_INTERLEAVED if interleaved else 0) | (PKV_ROPE_CYCLIC_AXES if cyclic_axes else 0)
-    f16, lib, st = torch.float16, _lib or load_library(), _raw_stream(stream, torch, device)
+    f16, lib, st = torch.float16, _lib, _raw_stream(stream, device)
     head = (_take("q_out", q_out, f16, rows, device), _take("q", q, f16, rows, device),
             _take("k_new", k_new, f16, kv_rows, device), _take("v_new", v_new, f16, kv_rows, device), kc, vc)
     sizes = (_take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device),
@@ -585,15 +600,15 @@ def paged_gqa_decode_attention_int8(out, q, k_cache, v_cache, kv_scales, block_t
                                     max_context_len, softmax_scale, workspace, stream=None) -> None:
     """paged_gqa_decode_attention over an 8-bit cache (load-balanced plan; a zero-filled workspace of
     paged_gqa_decode_workspace_size_int8() bytes, reusable)."""
-    import torch
-    device = torch.cuda.current_device()
+    torch = _torch or _runtime()
+    device = _current_device()
     args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
         out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
     if n != B:
         raise ValueError(f"{n} query rows for {B} sequences")
-    _check((_lib or load_library()).paged_gqa_decode_attention_int8(
+    _check(_lib.paged_gqa_decode_attention_int8(
         *args, B, Hq, Hkv, D, bs, mb, NB, max_context_len, softmax_scale, ws, ws_bytes,
-        _raw_stream(stream, torch, device)), "paged_gqa_decode_attention_int8")
+        _raw_stream(stream, device)), "paged_gqa_decode_attention_int8")
 
 
 def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, *,
@@ -601,11 +616,11 @@ def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_
     """paged_gqa_prefill_attention over an 8-bit cache: query rows q [total, Hq, D] of each sequence
     (query_start [B+1] int32), the last n_b tokens of its context, attending causally; a zero-filled
     workspace of paged_gqa_prefill_workspace_size(Hq, Hkv, D, "int8") bytes, reusable."""
-    import torch
-    device = torch.cuda.current_device()
+    torch = _torch or _runtime()
+    device = _current_device()
     args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
         out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
-    _check((_lib or load_library()).paged_gqa_prefill_attention_int8(
+    _check(_lib.paged_gqa_prefill_attention_int8(
         *args, _take("query_start", query_start, torch.int32, (B + 1,), device), B, n, max_query_len, Hq, Hkv, D, bs,
-        mb, NB, max_context_len, softmax_scale, ws, ws_bytes, _raw_stream(stream, torch, device)),
+        mb, NB, max_context_len, softmax_scale, ws, ws_bytes, _raw_stream(stream, device)),
         "paged_gqa_prefill_attention_int8")
