@@ -825,17 +825,17 @@ int device_sms() {
 // Workspace of the 8-bit attention kernels: the merge tickets first, at the
 // same place whatever the kernel (they are zero between calls, so calls of
 // every kind can share a workspace), then the pieces' partial results: (m, l)
-// and O of two pieces per worker warp (streaming), or of two pieces x two
-// softmax streams per CTA (tensor-core chunks).
+// and O of a piece per worker warp and two items per CTA (streaming), or of two
+// pieces x two softmax streams per CTA (tensor-core chunks).
 struct Int8Workspace {
     size_t tickets, ml, o, stream_total, parts, total;
 };
 Int8Workspace int8_workspace(int sms) {
-    const size_t slots = 2 * (size_t)sms * kStreamWarps;
+    const size_t slots = (size_t)sms * (kStreamWarps + 2);
     Int8Workspace w;
     w.tickets = 0;
-    w.ml = align256(pkv::kMergeLevels * slots * sizeof(unsigned int));
-    static_assert(pkv::kMergeLevels * 2 * kStreamWarps >= 2 * 4, "tickets of a CTA's two streams x four warps fit");
+    // the larger of [levels][2 CTAs] (streaming) and [CTAs][2 streams][4 warps] (chunks)
+    w.ml = align256((size_t)sms * std::max(pkv::kTreeLevels * 2, 2 * 4) * sizeof(unsigned int));
     w.o = w.ml + align256(slots * 4 * sizeof(float4));
     w.stream_total = w.o + slots * 256 * sizeof(float4);
     w.parts = w.ml;

@@ -2,12 +2,20 @@
 // (int8_cache.cuh), load-balanced streaming form: decode (one query token per
 // sequence), and chunks whose query tokens x heads fit eight columns.
 //
-// Work is cut as in decode_balanced.cuh: a unit is one page (16 tokens) of one
-// KV head of one sequence; the units of the batch form a row, every warp of
-// the persistent grid takes an equal run of it, streams its pages through its
-// own ring of TMA copies, and the pieces of a segment (sequence, KV head) that
-// was cut between warps are merged by a fan-in-32 ticket tree. Nothing waits
-// on another CTA.
+// A unit is one page (16 tokens) of one KV head of one sequence; the units of
+// the batch form a row, and every warp of the persistent grid takes an equal
+// run of it and streams its pages through its own ring of TMA copies. A
+// segment (sequence, KV head) that lies in one warp's run is written by that
+// warp. The pieces of the others are merged at the end of the CTA's run: a
+// warp leaves the piece its run ends in in its (then free) ring, the piece its
+// run began in in the workspace, and after a barrier each chain of pieces of
+// one segment is merged by one warp. A chain that is the whole segment is
+// written; one that reaches into other CTAs becomes an item of a ticket tree
+// of fan-in 16, whose last arrival at each node merges it, staging the items'
+// 64 KiB through the ring in one round trip. Nothing waits on another CTA.
+// (With the pieces merged through the workspace warp by warp instead, in a
+// fan-in-32 tree as decode_balanced.cuh does, the 64-sequence decode took
+// 24.1 us and the skewed one 30.2 us, most of it in the merges.)
 //
 // Columns: the N = 8 side of the tensor-core products (mma.sync m16n8k16,
 // tokens on M) holds (query token, head of the KV head's group), column =
@@ -43,9 +51,11 @@ struct StreamInt8Params {
     const int32_t* block_tables;  // [B, max_blocks_per_seq]
     const int32_t* context_lens;  // [B]
     const int32_t* query_start;   // [B + 1], or null: one query per sequence (decode)
-    float4* ws_o;                 // [2 * workers][8][32 lanes]  pieces' unnormalised O
-    float4* ws_ml;                // [2 * workers][4]  (m, l) of columns 2c, 2c + 1
-    unsigned int* ws_count;       // tickets of the merge tree, zero between calls
+    // partial results: unnormalised O and (m, l) of columns 2c, 2c + 1, of the pieces that workers' runs
+    // begin in, then of two items per CTA (a segment that began in an earlier CTA; one that began here)
+    float4* ws_o;                 // [workers + 2 CTAs][8][32 lanes]
+    float4* ws_ml;                // [workers + 2 CTAs][4]
+    unsigned int* ws_count;       // [kTreeLevels][2 CTAs] tickets of the merge tree, zero between calls
     int32_t B, Hq, Hkv, G;
     int32_t total, max_query_len;
     int32_t max_blocks_per_seq, num_blocks, max_context_len;
@@ -57,6 +67,8 @@ constexpr float kScaleMax = 1.152921504606846976e18f;      // 2^60
 constexpr float kScaleMin = 8.673617379884035472e-19f;     // 2^-60
 constexpr float kStreamRaise = 6.f;                        // log2 of the largest weight
 constexpr float kLogitFloor = -1e30f;                      // stands in for a maximum of -inf
+constexpr int kTreeFan = 16;                               // items a node of the cross-CTA tree merges
+constexpr int kTreeLevels = 3;                             // 16^3 CTAs
 
 template <int kWarps, int kStages>
 struct StreamInt8Shape {
@@ -65,7 +77,12 @@ struct StreamInt8Shape {
     static constexpr int kScaleBytes = 128;                 // K scales, V scales of the page
     static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
     static constexpr int kScaleRing = kWarps * kStages * kScaleBytes;
-    static constexpr int kMergeBytes = kWarps * kMergeFloats * 4;
+    static constexpr int kMergeFloats = 32 * 8 + 16;        // per warp: weights of up to 32 items x 8 columns, M, L
+    static constexpr int kTailBytes = kWarps * 4 * 16;      // (m, l) of the pieces the warps' runs end in
+    static constexpr int kSegBytes = kWarps * 2 * 4;        // segment of every warp's first and last piece, or -1
+    static constexpr int kMergeBytes = (kWarps * kMergeFloats * 4 + kTailBytes + kSegBytes + 15) / 16 * 16;
+    static constexpr int kStageItems = kRingBytes / 2 / 4096;   // items half the ring can hold
+    static_assert(2 * kWarps <= 32 && kStageItems >= kTreeFan, "chains and tree nodes fit one warp's lanes and staging");
     static constexpr int kBarBytes = kWarps * kStages * 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kFixed = 1024 + kRingBytes + kScaleRing + kMergeBytes + kBarBytes;
@@ -102,7 +119,9 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t ring = (raw + 1023u) & ~1023u;
     const uint32_t scale_ring = ring + S::kRingBytes;
     uint8_t* after = smem_raw + (ring - raw) + S::kRingBytes + S::kScaleRing;
-    float* wts = reinterpret_cast<float*>(after) + warp * kMergeFloats;    // [32 items][8 columns], M[8], L[8]
+    float* wts = reinterpret_cast<float*>(after) + warp * S::kMergeFloats;   // [32 items][8 columns], M[8], L[8]
+    float4* tail_ml = reinterpret_cast<float4*>(after + kWarps * S::kMergeFloats * 4);              // [warps][4]
+    int* seg_of = reinterpret_cast<int*>(after + kWarps * S::kMergeFloats * 4 + S::kTailBytes);   // [warps][2]
     const uint32_t bars = scale_ring + S::kScaleRing + S::kMergeBytes;
     int* prefix = reinterpret_cast<int*>(after + S::kMergeBytes + S::kBarBytes);   // [B + 1]
 
@@ -176,7 +195,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int W = min(W_total, max(1, want));
     const int u0 = U == 0 ? 0 : (int)range_start(worker, U, W);
     const int n = (U == 0 || worker >= W) ? 0 : (int)range_start(worker + 1, U, W) - u0;
-    if (n <= 0) return;
+    if (lane < 2) seg_of[2 * warp + lane] = -1;
     if (lane == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -235,10 +254,10 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
     // ---- the current segment: KV head g of sequence b; page j of nb ----
     const int r = lane >> 2, c = lane & 3;
-    int b = seq_of_unit(prefix, B, u0);
-    int nb = pages_of(b);
-    int g = (u0 - prefix[b]) / nb;
-    int j = (u0 - prefix[b]) - g * nb;
+    int b = n > 0 ? seq_of_unit(prefix, B, u0) : 0;
+    int nb = n > 0 ? pages_of(b) : 1;
+    int g = n > 0 ? (u0 - prefix[b]) / nb : 0;
+    int j = n > 0 ? (u0 - prefix[b]) - g * nb : 0;
     int piece_j0 = j;
     int row0 = 0, ncols = 0;                     // the sequence's first row of q and out; live columns
     int lim_lo = 0, lim_hi = 0;                  // positions of its first and last query
@@ -263,7 +282,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             qf[kk][1] = v.y;
         }
     };
-    open_segment();
+    if (n > 0) open_segment();
 
     float m[2], l[2], o[8][4];                   // columns 2c, 2c + 1: running maximum, sum, output
     auto reset = [&]() {
@@ -392,16 +411,8 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             for (int i = 0; i < 8; ++i) dst[8 * i + r] = __floats2half2_rn(v[i][e] * inv, v[i][2 + e] * inv);
         }
     };
-    // (m, l, O) of one partial result, in fragment order, at workspace slot `slot`
-    auto store_item = [&](int slot, const float (&v)[8][4], float m0, float l0, float m1, float l1) {
-        float4* dst = p.ws_o + (int64_t)slot * 256 + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) __stcg(dst + 32 * i, make_float4(v[i][0], v[i][1], v[i][2], v[i][3]));
-        if (r == 0) __stcg(p.ws_ml + (int64_t)slot * 4 + c, make_float4(m0, l0, m1, l1));
-    };
-
-    // Finishes the piece of the current segment whose last page is j_last.
-    auto finish_piece = [&](int j_last) {
+    // Writes or puts aside the piece of the current segment whose last page is j_last.
+    auto finish_piece = [&](int j_last, bool at_end) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
@@ -411,97 +422,25 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             write_out(o, 1.f / l[0], 1.f / l[1]);
             return;
         }
-        const int seg_first = prefix[b] + g * nb;
-        const int k_first = worker_of(seg_first, U, W);
-        const int k_last = worker_of(seg_first + nb - 1, U, W);
-        auto slot_of_piece = [&](int q) {
-            const int k = k_first + q;
-            return 2 * k + (range_start(k, U, W) >= seg_first ? 0 : 1);
-        };
-        int item = worker - k_first, n_items = k_last - k_first + 1, span = 1;
-        store_item(slot_of_piece(item), o, m[0], l[0], m[1], l[1]);
-        for (int lvl = 0;; ++lvl) {
-            const int first = item - item % kMergeFan, last = min(first + kMergeFan, n_items) - 1;
-            const int cslot = slot_of_piece(first * span);
-            unsigned int* cnt = p.ws_count + (int64_t)lvl * 2 * W_total + cslot;
-            // the warp barrier orders every lane's stores before lane 0's release-acquire ticket;
-            // the merger's loads follow its acquire
-            __syncwarp();
-            unsigned int prev = 0;
-            if (lane == 0) prev = atomic_add_acq_rel_gpu(cnt, 1u);
-            prev = __shfl_sync(0xffffffffu, prev, 0);
-            if (prev != (unsigned int)(last - first)) return;   // another item merges the group
-            const int n_it = last - first + 1;
-            const int my_slot = lane < n_it ? slot_of_piece((first + lane) * span) : 0;
-            const int n_next = (n_items + kMergeFan - 1) / kMergeFan;
-            auto load_vals = [&](float4 (&dst)[2][8], int k) {
+        // the piece a run ends in stays in the ring (free by now), the piece it began in goes to the workspace
+        const float4 ml = make_float4(m[0], l[0], m[1], l[1]);
+        if (at_end) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (k + u < n_it) {
-                        const int slot = __shfl_sync(0xffffffffu, my_slot, k + u);
-                        const float4* src = p.ws_o + (int64_t)slot * 256 + lane;
+            for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(k_tile(0) + 512 * i + 16 * lane),
+                             "f"(o[i][0]), "f"(o[i][1]), "f"(o[i][2]), "f"(o[i][3]) : "memory");
+            if (r == 0) tail_ml[4 * warp + c] = ml;
+        } else {
+            float4* dst = p.ws_o + (int64_t)worker * 256 + lane;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[u][i] = __ldcg(src + 32 * i);
-                    }
-            };
-            float4 va[2][8];
-            load_vals(va, 0);
-            float mm[8], ll[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float4 a = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                if (lane < n_it) a = __ldcg(p.ws_ml + (int64_t)my_slot * 4 + k);
-                mm[2 * k] = a.x; ll[2 * k] = a.y; mm[2 * k + 1] = a.z; ll[2 * k + 1] = a.w;
-            }
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                float M = mm[h];
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-                const float w = fast_exp2(mm[h] - fmaxf(M, kLogitFloor));   // 0 for an item that saw nothing
-                float L = w * ll[h];
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-                wts[lane * 8 + h] = w;
-                if (lane == 0) {
-                    wts[256 + h] = M;
-                    wts[264 + h] = L;
-                }
-            }
-            __syncwarp();
-            float acc[8][4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll 1
-            for (int k = 0; k < n_it; k += 2) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (k + u < n_it) {
-                        const float w0 = wts[(k + u) * 8 + 2 * c], w1 = wts[(k + u) * 8 + 2 * c + 1];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            acc[i][0] += w0 * va[u][i].x; acc[i][1] += w1 * va[u][i].y;
-                            acc[i][2] += w0 * va[u][i].z; acc[i][3] += w1 * va[u][i].w;
-                        }
-                    }
-                if (k + 2 < n_it) load_vals(va, k + 2);
-            }
-            const float M0 = wts[256 + 2 * c], M1 = wts[256 + 2 * c + 1];
-            const float L0 = wts[264 + 2 * c], L1 = wts[264 + 2 * c + 1];
-            __syncwarp();
-            if (lane == 0) *cnt = 0u;                             // ready for the next call
-            if (n_next == 1) {
-                write_out(acc, 1.f / L0, 1.f / L1);
-                return;
-            }
-            store_item(cslot, acc, M0, L0, M1, L1);               // the group is one item of the next level
-            item = first / kMergeFan;
-            n_items = n_next;
-            span *= kMergeFan;
+            for (int i = 0; i < 8; ++i) __stcg(dst + 32 * i, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
+            if (r == 0) __stcg(p.ws_ml + (int64_t)worker * 4 + c, ml);
         }
+        if (lane == 0) seg_of[2 * warp + (at_end ? 1 : 0)] = b * Hkv + g;
     };
 
-    // A wait that ran out (flagged) ends this worker, after the copies it issued have landed.
+    // A wait that ran out (flagged) ends this worker's run, after the copies it issued have landed. Its
+    // pieces are not merged; the workspace's tickets must be cleared.
     auto drain_after = [&](int lost) {
         for (int u = lost + 1; u < issued; ++u) mbar_wait(full_bar(u % kStages), (u / kStages) & 1);
     };
@@ -509,13 +448,13 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const int s = t % kStages;
         if (!__all_sync(0xffffffffu, mbar_wait(full_bar(s), (t / kStages) & 1))) {
             drain_after(t);
-            return;
+            break;
         }
         if (j + 1 < nb && t + 1 < n) {           // two pages of the segment in one softmax step
             const int s2 = (t + 1) % kStages;
             if (!__all_sync(0xffffffffu, mbar_wait(full_bar(s2), ((t + 1) / kStages) & 1))) {
                 drain_after(t + 1);
-                return;
+                break;
             }
             attend(std::integral_constant<int, 2>(), s, s2, j);
             __syncwarp();
@@ -530,22 +469,184 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         const bool seg_end = j == nb - 1;
         if (seg_end || t == n - 1) {
-            finish_piece(j);
+            finish_piece(j, t == n - 1);
             if (t == n - 1) break;
-            // (a range's last unit always closes a piece, so here the segment ended)
+            // (a run's last unit always closes a piece, so here the segment ended)
             j = 0;
             if (++g == Hkv) {
                 g = 0;
                 do { ++b; } while (prefix[b + 1] == prefix[b]);
                 nb = pages_of(b);
             }
-            __syncwarp();
             open_segment();
             reset();
             piece_j0 = 0;
         } else {
             ++j;
         }
+    }
+
+    // ---- the CTA's pieces, in the order of its run: piece 2 w (the one warp w's run began in) and
+    // 2 w + 1 (the one it ended in), where they exist; pieces of one segment are neighbours ----
+    __syncthreads();
+    const int my_seg = lane < 2 * kWarps ? seg_of[lane] : -1;
+    const unsigned pieces = __ballot_sync(0xffffffffu, my_seg >= 0);
+    const unsigned before = pieces & ((1u << lane) - 1u);
+    const int prev_seg = __shfl_sync(0xffffffffu, my_seg, before ? 31 - __clz(before) : 0);
+    unsigned starts = __ballot_sync(0xffffffffu, my_seg >= 0 && (before == 0 || prev_seg != my_seg));
+    const int n_chains = __popc(starts);
+    const int cta_lo = (int)range_start(min((int)blockIdx.x * kWarps, W), U, W);
+    const int cta_hi = (int)range_start(min(((int)blockIdx.x + 1) * kWarps, W), U, W);
+    float acc[8][4];
+    // acc = sum of the items' O times their weights; wts holds the weights, M and L. `value`: a lane's eight
+    // float4 of an item; `ml`: this lane's item's (m, l) of columns 2k, 2k + 1.
+    auto weigh = [&](int n_it, auto ml) {
+        float mm[8], ll[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float4 a = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            if (lane < n_it) a = ml(k);
+            mm[2 * k] = a.x; ll[2 * k] = a.y; mm[2 * k + 1] = a.z; ll[2 * k + 1] = a.w;
+        }
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            float M = mm[h];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            const float w = fast_exp2(mm[h] - fmaxf(M, kLogitFloor));       // 0 for an item that saw nothing
+            float L = w * ll[h];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            wts[lane * 8 + h] = w;
+            if (lane == 0) {
+                wts[256 + h] = M;
+                wts[264 + h] = L;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    };
+    auto add_item = [&](int k, const float4 (&v)[8]) {
+        const float w0 = wts[k * 8 + 2 * c], w1 = wts[k * 8 + 2 * c + 1];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            acc[i][0] = fmaf(w0, v[i].x, acc[i][0]); acc[i][1] = fmaf(w1, v[i].y, acc[i][1]);
+            acc[i][2] = fmaf(w0, v[i].z, acc[i][2]); acc[i][3] = fmaf(w1, v[i].w, acc[i][3]);
+        }
+    };
+    auto load_shared_item = [&](uint32_t addr, float4 (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 u = lds128(addr + 512 * i + 16 * lane);
+            v[i] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+        }
+    };
+    const int item0 = gridDim.x * kWarps;                       // the CTAs' items lie behind the workers' pieces
+    auto publish = [&](int slot) {
+        float4* dst = p.ws_o + (int64_t)slot * 256 + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) __stcg(dst + 32 * i, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
+        if (r == 0)
+            __stcg(p.ws_ml + (int64_t)slot * 4 + c,
+                   make_float4(wts[256 + 2 * c], wts[264 + 2 * c], wts[257 + 2 * c], wts[265 + 2 * c]));
+    };
+    int half = -1, seg_first = 0;                               // this warp's item of the CTA: 0, 1 or none
+    for (int k = 0; k < n_chains; ++k) {
+        const int first = __ffs(starts) - 1;
+        starts &= starts - 1;
+        // a warp each; of kWarps + 1 chains (every boundary between warps cuts a segment) the last warp takes
+        // two, of which the first lies inside the CTA
+        if (min(k, kWarps - 1) != warp) continue;
+        // the chain: the pieces from `first` up to the next chain
+        const unsigned chain = pieces & ~((1u << first) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
+        const int n_it = __popc(chain);
+        const int seg = __shfl_sync(0xffffffffu, my_seg, first);
+        b = seg / Hkv;
+        g = seg - b * Hkv;
+        nb = pages_of(b);
+        open_segment();
+        const int sf = prefix[b] + g * nb;
+        // lane q's piece, 2 w or 2 w + 1: the q-th set bit of the chain
+        unsigned rest = chain;
+        for (int q = 0; q < lane && q < n_it; ++q) rest &= rest - 1;
+        const int piece = lane < n_it ? __ffs(rest) - 1 : 0;
+        weigh(n_it, [&](int e) {
+            return (piece & 1) ? tail_ml[4 * (piece >> 1) + e]
+                               : __ldcg(p.ws_ml + (int64_t)(blockIdx.x * kWarps + (piece >> 1)) * 4 + e);
+        });
+        for (int q = 0; q < n_it; ++q) {
+            const int pq = __shfl_sync(0xffffffffu, piece, q), w = pq >> 1;
+            float4 v[8];
+            if (pq & 1) {
+                load_shared_item(ring + w * kStages * S::kSlotBytes, v);
+            } else {
+                const float4* src = p.ws_o + (int64_t)(blockIdx.x * kWarps + w) * 256 + lane;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + 32 * i);
+            }
+            add_item(q, v);
+        }
+        if (sf >= cta_lo && sf + nb <= cta_hi) {
+            write_out(acc, 1.f / wts[264 + 2 * c], 1.f / wts[265 + 2 * c]);
+        } else {
+            half = sf >= cta_lo ? 1 : 0;
+            seg_first = sf;
+            publish(item0 + 2 * blockIdx.x + half);
+        }
+        __syncwarp();
+    }
+    __syncthreads();                                            // the ring is free
+    if (half < 0) return;
+
+    // ---- the ticket tree over the CTAs' items of this segment ----
+    const int c_first = worker_of(seg_first, U, W) / kWarps;
+    int n_items = worker_of(seg_first + nb - 1, U, W) / kWarps - c_first + 1;
+    int item = blockIdx.x - c_first, span = 1;
+    auto slot_of_item = [&](int q) {                             // 2 c + 1 where the segment began in CTA c
+        const int cc = c_first + q;
+        return 2 * cc + (range_start(cc * kWarps, U, W) <= seg_first ? 1 : 0);
+    };
+    const uint32_t stage = ring + half * (S::kStageItems * 4096);
+    for (int lvl = 0;; ++lvl) {
+        const int first = item - item % kTreeFan, last = min(first + kTreeFan, n_items) - 1;
+        const int cslot = slot_of_item(first * span);
+        unsigned int* cnt = p.ws_count + (int64_t)lvl * 2 * gridDim.x + cslot;
+        // the warp barrier orders every lane's stores before lane 0's release-acquire ticket; the
+        // merger's loads follow its acquire
+        __syncwarp();
+        unsigned int prev = 0;
+        if (lane == 0) prev = atomic_add_acq_rel_gpu(cnt, 1u);
+        prev = __shfl_sync(0xffffffffu, prev, 0);
+        if (prev != (unsigned int)(last - first)) return;       // another item merges the node
+        if (lane == 0) *cnt = 0u;                               // ready for the next call
+        const int n_it = last - first + 1;
+        const int my_slot = item0 + (lane < n_it ? slot_of_item((first + lane) * span) : 0);
+        for (int q = 0; q < n_it; ++q) {
+            const int slot = __shfl_sync(0xffffffffu, my_slot, q);
+            const float4* src = p.ws_o + (int64_t)slot * 256 + lane;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cp_async16(stage + q * 4096 + 512 * i + 16 * lane, src + 32 * i);
+        }
+        cp_async_commit();
+        weigh(n_it, [&](int e) { return __ldcg(p.ws_ml + (int64_t)my_slot * 4 + e); });
+        cp_async_wait_all();
+        __syncwarp();
+        for (int q = 0; q < n_it; ++q) {
+            float4 v[8];
+            load_shared_item(stage + q * 4096, v);
+            add_item(q, v);
+        }
+        const int n_next = (n_items + kTreeFan - 1) / kTreeFan;
+        if (n_next == 1) {
+            write_out(acc, 1.f / wts[264 + 2 * c], 1.f / wts[265 + 2 * c]);
+            return;
+        }
+        publish(item0 + cslot);                                 // the node is one item of the next level
+        __syncwarp();
+        item = first / kTreeFan;
+        n_items = n_next;
+        span *= kTreeFan;
     }
 }
 

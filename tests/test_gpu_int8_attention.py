@@ -128,6 +128,26 @@ def test_decode_many_short_sequences():
     c.check(c.decode(), "many")
 
 
+def test_decode_cuts_at_every_warp():
+    """Segments about as long as a warp's run: every run begins and ends inside one, so a CTA merges one
+    chain more than it has warps, and both its first and its last reach into other CTAs."""
+    rng = np.random.default_rng(55)
+    c = Case(55, 2, 1, list(rng.integers(150, 230, 1100)))
+    ws = workspace()
+    got = c.decode(ws)
+    c.check(got, "cuts")
+    assert np.array_equal(got, c.decode(ws))
+
+
+def test_decode_one_sequence_over_the_whole_grid():
+    """One long sequence and one head: its pieces meet in a ticket tree of two levels."""
+    c = Case(56, 1, 1, [40000])
+    ws = workspace()
+    got = c.decode(ws)
+    c.check(got, "whole grid")
+    assert np.array_equal(got, c.decode(ws)) and (ws[:1 << 12] == 0).all()
+
+
 @pytest.mark.parametrize("kind", ["large logits", "zero scale", "negative scale", "tiny values", "huge values",
                                   "zero rows", "mixed", "growing"])
 def test_decode_value_ranges(kind):
