@@ -858,7 +858,7 @@ bool stream_fits(int64_t B, int64_t Hkv, int64_t max_context_len) {
 // product tile of 8, over the 8-bit cache.
 pkv_status launch_stream_int8(pkv::StreamInt8Params prm, const void* k_cache, const void* v_cache,
                               const float* kv_scales, void* workspace, size_t workspace_bytes, cudaStream_t st) {
-    prm.min_units_per_worker = kBalMinUnits;
+    prm.min_units_per_worker = 1;
     const int sms = device_sms();
     if (sms <= 0) return PKV_ERR_CUDA;
     const Int8Workspace w = int8_workspace(sms);

@@ -77,12 +77,12 @@ struct StreamInt8Shape {
     static constexpr int kScaleBytes = 128;                 // K scales, V scales of the page
     static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
     static constexpr int kScaleRing = kWarps * kStages * kScaleBytes;
-    static constexpr int kMergeFloats = 32 * 8 + 16;        // per warp: weights of up to 32 items x 8 columns, M, L
+    static constexpr int kMergeFloats = 2 * 32 * 8 + 8;     // per warp: weights and weighted sums of 32 items x 8 columns, M
     static constexpr int kTailBytes = kWarps * 4 * 16;      // (m, l) of the pieces the warps' runs end in
     static constexpr int kSegBytes = kWarps * 2 * 4;        // segment of every warp's first and last piece, or -1
     static constexpr int kMergeBytes = (kWarps * kMergeFloats * 4 + kTailBytes + kSegBytes + 15) / 16 * 16;
     static constexpr int kStageItems = kRingBytes / 2 / 4096;   // items half the ring can hold
-    static_assert(2 * kWarps <= 32 && kStageItems >= kTreeFan, "chains and tree nodes fit one warp's lanes and staging");
+    static_assert(2 * kWarps <= 32 && kStageItems >= kTreeFan && kStages * kSlotBytes >= 3 * 4096, "chains and tree nodes fit one warp's lanes and staging");
     static constexpr int kBarBytes = kWarps * kStages * 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kFixed = 1024 + kRingBytes + kScaleRing + kMergeBytes + kBarBytes;
@@ -97,6 +97,12 @@ __device__ __forceinline__ float fast_log2(float x) {
 __device__ __forceinline__ float fast_rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Maximum over the warp (redux.sync takes fp32 on sm_100a; NaN is ignored).
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float lds32(uint32_t addr) {
@@ -119,7 +125,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t ring = (raw + 1023u) & ~1023u;
     const uint32_t scale_ring = ring + S::kRingBytes;
     uint8_t* after = smem_raw + (ring - raw) + S::kRingBytes + S::kScaleRing;
-    float* wts = reinterpret_cast<float*>(after) + warp * S::kMergeFloats;   // [32 items][8 columns], M[8], L[8]
+    float* wts = reinterpret_cast<float*>(after) + warp * S::kMergeFloats;   // [32 items][8 columns] x 2, M[8]
     float4* tail_ml = reinterpret_cast<float4*>(after + kWarps * S::kMergeFloats * 4);              // [warps][4]
     int* seg_of = reinterpret_cast<int*>(after + kWarps * S::kMergeFloats * 4 + S::kTailBytes);   // [warps][2]
     const uint32_t bars = scale_ring + S::kScaleRing + S::kMergeBytes;
@@ -223,7 +229,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     };
     int win_phys, win_head, nxt_phys, nxt_head, cur_win = 0;
     load_window(0, win_phys, win_head);
-    load_window(1, nxt_phys, nxt_head);
+    nxt_phys = -1, nxt_head = 0;                 // (the next window is looked up behind the first copies)
     const uint64_t policy = l2_evict_first_policy();             // a page is read once
     int issued = 0;                              // units [0, issued) have their copies in flight or landed
     auto issue = [&](int t) {
@@ -251,6 +257,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
     };
     for (int t = 0; t < min(n, kStages); ++t) issue(t);
+    load_window(1, nxt_phys, nxt_head);
 
     // ---- the current segment: KV head g of sequence b; page j of nb ----
     const int r = lane >> 2, c = lane & 3;
@@ -497,9 +504,9 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int n_chains = __popc(starts);
     const int cta_lo = (int)range_start(min((int)blockIdx.x * kWarps, W), U, W);
     const int cta_hi = (int)range_start(min(((int)blockIdx.x + 1) * kWarps, W), U, W);
-    float acc[8][4];
-    // acc = sum of the items' O times their weights; wts holds the weights, M and L. `value`: a lane's eight
-    // float4 of an item; `ml`: this lane's item's (m, l) of columns 2k, 2k + 1.
+    float acc[8][4], L0, L1;                                    // a merge's O, and sums of columns 2c, 2c + 1
+    // Starts a merge of n_it items, whose (m, l) of columns 2k, 2k + 1 lane q has for item q: their weights
+    // 2^(m - M) go to wts.
     auto weigh = [&](int n_it, auto ml) {
         float mm[8], ll[8];
 #pragma unroll
@@ -510,25 +517,22 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
-            float M = mm[h];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            const float M = warp_max(mm[h]);
             const float w = fast_exp2(mm[h] - fmaxf(M, kLogitFloor));       // 0 for an item that saw nothing
-            float L = w * ll[h];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
             wts[lane * 8 + h] = w;
-            if (lane == 0) {
-                wts[256 + h] = M;
-                wts[264 + h] = L;
-            }
+            wts[256 + lane * 8 + h] = w * ll[h];
+            if (lane == 0) wts[512 + h] = M;
         }
         __syncwarp();
+        L0 = L1 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     };
+    // adds item k, `v` being this lane's eight float4 of it
     auto add_item = [&](int k, const float4 (&v)[8]) {
         const float w0 = wts[k * 8 + 2 * c], w1 = wts[k * 8 + 2 * c + 1];
+        L0 += wts[256 + k * 8 + 2 * c];
+        L1 += wts[257 + k * 8 + 2 * c];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             acc[i][0] = fmaf(w0, v[i].x, acc[i][0]); acc[i][1] = fmaf(w1, v[i].y, acc[i][1]);
@@ -549,7 +553,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         for (int i = 0; i < 8; ++i) __stcg(dst + 32 * i, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
         if (r == 0)
             __stcg(p.ws_ml + (int64_t)slot * 4 + c,
-                   make_float4(wts[256 + 2 * c], wts[264 + 2 * c], wts[257 + 2 * c], wts[265 + 2 * c]));
+                   make_float4(wts[512 + 2 * c], L0, wts[513 + 2 * c], L1));
     };
     int half = -1, seg_first = 0;                               // this warp's item of the CTA: 0, 1 or none
     for (int k = 0; k < n_chains; ++k) {
@@ -588,7 +592,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             add_item(q, v);
         }
         if (sf >= cta_lo && sf + nb <= cta_hi) {
-            write_out(acc, 1.f / wts[264 + 2 * c], 1.f / wts[265 + 2 * c]);
+            write_out(acc, 1.f / L0, 1.f / L1);
         } else {
             half = sf >= cta_lo ? 1 : 0;
             seg_first = sf;
@@ -596,8 +600,21 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         __syncwarp();
     }
-    __syncthreads();                                            // the ring is free
-    if (half < 0) return;
+    // A merge of more than two items stages them through the ring, once every warp is done with the pieces
+    // in it; nobody else waits for that.
+    bool arrived = false;
+    auto leave_ring = [&]() {
+        if (!arrived) asm volatile("bar.arrive 1, %0;" :: "n"(S::kThreads) : "memory");
+        arrived = true;
+    };
+    auto take_ring = [&]() {
+        if (!arrived) asm volatile("bar.sync 1, %0;" :: "n"(S::kThreads) : "memory");
+        arrived = true;
+    };
+    if (half < 0) {
+        leave_ring();
+        return;
+    }
 
     // ---- the ticket tree over the CTAs' items of this segment ----
     const int c_first = worker_of(seg_first, U, W) / kWarps;
@@ -607,7 +624,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const int cc = c_first + q;
         return 2 * cc + (range_start(cc * kWarps, U, W) <= seg_first ? 1 : 0);
     };
-    const uint32_t stage = ring + half * (S::kStageItems * 4096);
+    bool whole_ring = false;                                    // the ring has been waited for
     for (int lvl = 0;; ++lvl) {
         const int first = item - item % kTreeFan, last = min(first + kTreeFan, n_items) - 1;
         const int cslot = slot_of_item(first * span);
@@ -618,9 +635,16 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         unsigned int prev = 0;
         if (lane == 0) prev = atomic_add_acq_rel_gpu(cnt, 1u);
         prev = __shfl_sync(0xffffffffu, prev, 0);
-        if (prev != (unsigned int)(last - first)) return;       // another item merges the node
+        if (prev != (unsigned int)(last - first)) {             // another item merges the node
+            leave_ring();
+            return;
+        }
         if (lane == 0) *cnt = 0u;                               // ready for the next call
         const int n_it = last - first + 1;
+        // two items fit behind this warp's own piece in its share of the ring
+        whole_ring = whole_ring || n_it > 2;
+        if (whole_ring) take_ring();
+        const uint32_t stage = whole_ring ? ring + half * (S::kStageItems * 4096) : k_tile(0) + 4096;
         const int my_slot = item0 + (lane < n_it ? slot_of_item((first + lane) * span) : 0);
         for (int q = 0; q < n_it; ++q) {
             const int slot = __shfl_sync(0xffffffffu, my_slot, q);
@@ -639,7 +663,8 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         const int n_next = (n_items + kTreeFan - 1) / kTreeFan;
         if (n_next == 1) {
-            write_out(acc, 1.f / wts[264 + 2 * c], 1.f / wts[265 + 2 * c]);
+            leave_ring();
+            write_out(acc, 1.f / L0, 1.f / L1);
             return;
         }
         publish(item0 + cslot);                                 // the node is one item of the next level
