@@ -74,13 +74,13 @@ struct ChunkInt8Shape {
     static constexpr int kOffRaw = kOffV + 2 * kTile;
     static constexpr int kOffScales = kOffRaw + 2 * kRaw;
     static constexpr int kOffBars = kOffScales + 2 * kScales;
-    static constexpr int kOffWords = kOffBars + kBarBytes;   // block scan [16], first sequence [2], abort flag
+    static constexpr int kOffWords = kOffBars + kBarBytes;   // block scan [20], first sequence [2], abort flag
     static constexpr int kSmemBytes = kOffWords + 256;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one SM");
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kConvertWarp = 8;              // 8..11
-    static constexpr int kTmaKWarp = 12, kTmaVWarp = 13, kMmaWarp = 14;
-    static constexpr int kThreads = 32 * 15;
+    static constexpr int kConvertWarp = 8;              // 8..11 K, 12..15 V
+    static constexpr int kTmaKWarp = 16, kTmaVWarp = 17, kMmaWarp = 18;
+    static constexpr int kThreads = 32 * 19;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr float kRescaleThreshold = 8.f;
     static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
@@ -122,6 +122,20 @@ __device__ __forceinline__ uint32_t times(uint32_t a, __half2 f) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 16 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        :: "r"(taddr), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+           "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+           "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+           "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+           "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+           "r"(__float_as_uint(v[15]))
+        : "memory");
+}
+
 template <bool kNarrow>
 __global__ void __launch_bounds__(ChunkInt8Shape::kThreads, 1)
 chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -139,8 +153,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         flag_error(PKV_DEVERR_WAIT_TIMEOUT);             // never seen: no operand tile could be addressed
         return;
     }
-    long long* s_red = reinterpret_cast<long long*>(smem_raw + S::kOffWords);     // [16]
-    long long* s_first = s_red + 16;                                              // [2]
+    long long* s_red = reinterpret_cast<long long*>(smem_raw + S::kOffWords);     // [20]
+    long long* s_first = s_red + 20;                                              // [2]
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_first + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.G, T = p.tokens;
@@ -298,7 +312,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t bars = base + S::kOffBars;
     const uint32_t q_full = bars, q_empty = bars + 8, drain = bars + 16;
     auto s_full = [&](int t) { return bars + 24 + 8u * t; };
-    auto p_full = [&](int t) { return bars + 40 + 8u * t; };
+    auto p_full = [&](int t, int h) { return bars + 40 + 8u * t + (h ? 192u : 0u); };   // halves of 64 tokens
     auto o_done = [&](int t) { return bars + 56 + 8u * t; };
     auto o_free = [&](int t) { return bars + 72 + 8u * t; };
     auto k_full = [&](int s) { return bars + 88 + 8u * s; };
@@ -311,7 +325,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     auto rv_empty = [&](int s) { return bars + 200 + 8u * s; };
     // narrow: the odd stream's (m, l) of a piece are in TMEM; the even stream has read them
     const uint32_t x_full = bars + 216, x_read = bars + 224;
-    const uint32_t tmem_slot = bars + 240;
+    const uint32_t tmem_slot = bars + 248;
     const int rows = G * T;                              // rows of Q the TMA fills; the rest stay zero
     if (threadIdx.x == 0) {
         *s_abort = 0;
@@ -322,7 +336,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         mbar_init(drain, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 128);
+            mbar_init(p_full(t, 0), 128);
+            mbar_init(p_full(t, 1), 128);
             mbar_init(o_done(t), 1);
             mbar_init(o_free(t), 128);
             mbar_init(k_full(t), 4);
@@ -330,7 +345,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             mbar_init(v_full(t), 4);
             mbar_init(v_empty(t), 1);
             mbar_init(rk_full(t), 1);
-            mbar_init(rk_empty(t), 4);
+            mbar_init(rk_empty(t), 8);                   // the V warps read their scales there too
             mbar_init(rv_full(t), 1);
             mbar_init(rv_empty(t), 4);
         }
@@ -435,9 +450,10 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // nothing of ours may be in flight when the CTA leaves
         for (int j = max(0, gj - kRawStages); j < gj; ++j) mbar_wait(full(j % kRawStages), (j / kRawStages) & 1);
         if (is_k && k >= 1) mbar_wait(q_full, (k - 1) & 1);
-    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + 4) {
-        // ========================= codes to f16 tiles: a token per thread =========================
-        const int row = 32 * (warp - S::kConvertWarp) + lane;      // token of the KV tile
+    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + 8) {
+        // =============== codes of K (four warps) and of V (four) to f16 tiles: a token per thread ===============
+        const bool is_k = warp < S::kConvertWarp + 4;
+        const int row = 32 * (warp & 3) + lane;                    // token of the KV tile
         const uint32_t sw = (uint32_t)(row & 7);
         // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`, 64 channels at
         // a time (kept as a loop: the roles' code competes for the instruction cache)
@@ -477,30 +493,25 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             if (live && !fine) flag_error(PKV_DEVERR_SCALE);
             return live && fine ? fminf(s, 511.75f) : 0.f;
         };
-        const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4);
+        const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4) + (is_k ? 0u : 64u);
+        const float sign = is_k ? p.key_sign : 1.f;
+        auto tile_empty = [&](int d) { return is_k ? k_empty(d) : v_empty(d); };
         Cursor cu = start;
         Piece pc;
-        int gj = 0;                                                // KV tiles of earlier pieces
-        float v_scale[2] = {0.f, 0.f};                             // of the tiles whose K is converted, V not yet
+        int g = 0;                                                 // KV tiles so far
         bool ok = true;
         while (ok && next_piece(cu, pc)) {
-            // steps K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
-            const int n = pc.j1 - pc.j0;
-            for (int step = 0; step < 2 * n; ++step) {
-                const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
-                const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
-                const int g = gj + i, s = g % kRawStages, d = g & 1;
-                if (!(ok = wait_all(is_k ? rk_full(s) : rv_full(s), (g / kRawStages) & 1))) break;
-                float scale;
-                if (is_k) {
-                    scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
-                    const float vs = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
-                    if (d) v_scale[1] = vs;
-                    else v_scale[0] = vs;
-                } else {
-                    scale = d ? v_scale[1] : v_scale[0];
+            for (int j = pc.j0; j < pc.j1; ++j, ++g) {
+                const int s = g % kRawStages, d = g & 1;
+                // (the scales come with the codes of K)
+                if (!(ok = wait_all(rk_full(s), (g / kRawStages) & 1))) break;
+                const float scale = row_scale(pc, j, raw_sc(s) + sc_off) * sign;
+                if (!is_k) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rk_empty(s));
+                    if (!(ok = wait_all(rv_full(s), (g / kRawStages) & 1))) break;
                 }
-                if (g >= 2 && !(ok = wait_all(is_k ? k_empty(d) : v_empty(d), ((g >> 1) - 1) & 1))) break;
+                if (g >= 2 && !(ok = wait_all(tile_empty(d), ((g >> 1) - 1) & 1))) break;
                 convert(is_k ? raw_k(s) : raw_v(s), is_k ? k_s(d) : v_s(d), scale);
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -509,7 +520,6 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     mbar_arrive(is_k ? k_full(d) : v_full(d));
                 }
             }
-            gj += n;
         }
     } else if (warp == S::kMmaWarp) {
         // ===================================== MMA =====================================
@@ -537,18 +547,24 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         };
         // O_t += P_t V(gg); `first`: the piece's first product on the stream overwrites O_t
         auto issue_pv = [&](int t, int gg, int cnt, bool free_v, bool first) -> bool {
-            if (!wait_all(p_full(t), cnt & 1)) return false;
-            tc_fence_after();
-            if (lane == 0) {
-                const int s = gg & 1;
+            const int s = gg & 1;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {                // as each half of P (64 tokens) comes in
+                if (!wait_all(p_full(t, h), cnt & 1)) return false;
+                tc_fence_after();
+                if (lane == 0) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_f16_ts(tmem_o(t), tmem_s(t) + 8 * kk, umma_desc_sw128(v_s(s) + kk * 2048, S::kChunk, 1024),
-                                kIdescPV, (!first || kk > 0) ? 1u : 0u);
-                umma_commit(o_done(t));
-                if (free_v) umma_commit(v_empty(s));
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ts(tmem_o(t), tmem_s(t) + 32 * h + 8 * kk,
+                                    umma_desc_sw128(v_s(s) + (4 * h + kk) * 2048, S::kChunk, 1024), kIdescPV,
+                                    (!first || h + kk > 0) ? 1u : 0u);
+                    if (h == 1) {
+                        umma_commit(o_done(t));
+                        if (free_v) umma_commit(v_empty(s));
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
             return true;
         };
         int gj = 0, k = 0;
@@ -629,29 +645,26 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int i = 0; i < mine; ++i, ++cnt) {
                 if (!(ok = wait_all(s_full(t), cnt & 1))) break;
                 if (idle) {                                      // no live row in this warp: P is not used
-                    mbar_arrive(p_full(t));
+                    mbar_arrive(p_full(t, 0));
+                    mbar_arrive(p_full(t, 1));
                     continue;
                 }
                 tc_fence_after();
                 const int t0 = (pc.j0 + (kNarrow ? 2 * i + t : i)) * S::kKvTok;
                 const bool edge = t0 + S::kKvTok - 1 > first_pos;
+                // pass 1: the row's maximum, 32 columns at a time (loops, not unrolled code: see the conversion)
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    float x[2][32];
-                    tmem_ld32x2(s_row + 64 * h, x[0], s_row + 64 * h + 32, x[1]);
+                for (int c = 0; c < 4; ++c) {
+                    float x[32];
+                    tmem_ld32(s_row + 32 * c, x);
+                    if (edge) {
+                        const int left = prow - t0 - 32 * c;     // the last of these columns in the row's reach
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2) {
-                        const int c = 2 * h + c2;
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                mx[e & 3] = fmaxf(mx[e & 3], t0 + 32 * c + e <= prow ? x[c2][e] : -INFINITY);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[c2][e]);
-                        }
+                        for (int e = 0; e < 32; ++e) x[e] = e <= left ? x[e] : -INFINITY;
                     }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
                 }
                 float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 mt = mt > -INFINITY ? mt * sl : -INFINITY;       // (a zero scale must not make -inf * 0)
@@ -674,32 +687,31 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const float m_use = fmaxf(m_run, kLogitFloor);   // (a row that has seen nothing: all weights 0)
                 float lt[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    float w[32];
-                    float xx[2][32];
-                    tmem_ld32x2(s_row + 64 * h, xx[0], s_row + 64 * h + 32, xx[1]);
+                for (int c = 0; c < 4; ++c) {
+                    float x[32], w[16];
+                    tmem_ld32(s_row + 32 * c, x);
+                    if (edge) {
+                        const int left = prow - t0 - 32 * c;
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2) {
-                        const int c = 2 * h + c2;
-                        const float (&x)[32] = xx[c2];
+                        for (int e = 0; e < 32; ++e) x[e] = e <= left ? fmaf(x[e], sl, -m_use) : -INFINITY;
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float e0 = fmaf(x[2 * e], sl, -m_use), e1 = fmaf(x[2 * e + 1], sl, -m_use);
-                            if (edge) {
-                                e0 = t0 + 32 * c + 2 * e <= prow ? e0 : -INFINITY;
-                                e1 = t0 + 32 * c + 2 * e + 1 <= prow ? e1 : -INFINITY;
-                            }
-                            const uint32_t pw = pack_half2(fast_exp2(e0), fast_exp2(e1));
-                            lt[e & 3] = add_f16_hi(add_f16_lo(lt[e & 3], pw), pw);
-                            w[16 * c2 + e] = __uint_as_float(pw);
-                        }
+                        for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], sl, -m_use);
                     }
-                    tmem_st32(s_row + 32 * h, w);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t pw = pack_half2(fast_exp2(x[2 * e]), fast_exp2(x[2 * e + 1]));
+                        lt[e & 3] = add_f16_hi(add_f16_lo(lt[e & 3], pw), pw);
+                        w[e] = __uint_as_float(pw);
+                    }
+                    tmem_st16(s_row + 16 * c, w);                // P over logits already read
+                    if (c & 1) {                                 // a half of P is in place (and O rescaled)
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(p_full(t, c >> 1));
+                    }
                 }
                 l_run += (lt[0] + lt[1]) + (lt[2] + lt[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(p_full(t));
             }
             if (!ok) break;
             if (!(ok = wait_all(o_done(t), (cnt - 1) & 1))) break;
@@ -816,31 +828,29 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll 1
             for (int c = c_first; c <= c_last; ++c) M = fmaxf(M, ml_of(c).x);
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {                        // 64 channels at a time
-                float o[2][32];
+            for (int h = 0; h < 4; ++h) {                        // 32 channels at a time
+                float o[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0.f;
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 den = 0.f;
 #pragma unroll 1
                 for (int c = c_first; c <= c_last; ++c) {
-                    const float4* src = reinterpret_cast<const float4*>(part_of(c)) + 16 * h * 128 + r;
-                    float4 v[16];
+                    const float4* src = reinterpret_cast<const float4*>(part_of(c)) + 8 * h * 128 + r;
+                    float4 v[8];
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] = __ldcg(src + q * 128);
+                    for (int q = 0; q < 8; ++q) v[q] = __ldcg(src + q * 128);
                     const float2 ml = ml_of(c);
                     const float w = fast_exp2(ml.x - M);         // 0 for a piece that saw no position of the row
                     den = fmaf(w, ml.y, den);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        float* d = &o[q >> 3][4 * (q & 7)];
-                        d[0] = fmaf(w, v[q].x, d[0]);
-                        d[1] = fmaf(w, v[q].y, d[1]);
-                        d[2] = fmaf(w, v[q].z, d[2]);
-                        d[3] = fmaf(w, v[q].w, d[3]);
+                    for (int q = 0; q < 8; ++q) {
+                        o[4 * q] = fmaf(w, v[q].x, o[4 * q]);
+                        o[4 * q + 1] = fmaf(w, v[q].y, o[4 * q + 1]);
+                        o[4 * q + 2] = fmaf(w, v[q].z, o[4 * q + 2]);
+                        o[4 * q + 3] = fmaf(w, v[q].w, o[4 * q + 3]);
                     }
                 }
-                store_out(2 * h, o[0], 1.f / den);
-                store_out(2 * h + 1, o[1], 1.f / den);
+                store_out(h, o, 1.f / den);
             }
         }
     }
