@@ -56,8 +56,8 @@ struct ChunkInt8Params {
     int32_t Hq, Hkv, G;
     int32_t max_blocks_per_seq, num_blocks, max_context_len;
     int32_t tokens;               // T: query tokens of a tile
-    float logit_scale_log2;       // |softmax_scale| * log2(e)
-    float key_sign;               // sign of softmax_scale, applied to the keys
+    float logit_scale_log2;       // |softmax_scale| * log2(e), or 1 when that is 0 (masked logits are -inf)
+    float key_sign;               // sign of softmax_scale (0 for 0), applied to the keys
 };
 
 struct ChunkInt8Shape {
@@ -120,6 +120,36 @@ __device__ __forceinline__ void dequant4(uint32_t w, const RowScale& s, uint32_t
 __device__ __forceinline__ uint32_t times(uint32_t a, __half2 f) {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Packed fp32 pairs: one instruction for two lanes of arithmetic.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// 32 logits of consecutive tokens, those past number `left` hidden.
+__device__ __forceinline__ void mask_past(float (&x)[32], int left) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = e <= left ? x[e] : -INFINITY;
 }
 
 // 16 32-bit TMEM columns of this thread's lane.
@@ -658,16 +688,11 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int c = 0; c < 4; ++c) {
                     float x[32];
                     tmem_ld32(s_row + 32 * c, x);
-                    if (edge) {
-                        const int left = prow - t0 - 32 * c;     // the last of these columns in the row's reach
+                    if (edge) mask_past(x, prow - t0 - 32 * c);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = e <= left ? x[e] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+                    for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
-                float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                mt = mt > -INFINITY ? mt * sl : -INFINITY;       // (a zero scale must not make -inf * 0)
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
                 const bool raise = mt > m_run + S::kRescaleThreshold;
                 const float m_new = raise ? mt : m_run;
                 // O_t is final for this tile: its last product completed before this S was issued
@@ -685,24 +710,24 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 m_run = m_new;
                 const float m_use = fmaxf(m_run, kLogitFloor);   // (a row that has seen nothing: all weights 0)
-                float lt[4] = {0.f, 0.f, 0.f, 0.f};
+                // pass 2: probabilities exp2(s * sl - m) to f16 for the products, and to the row sum before that
+                // rounding (its errors, half a step each, average out over the row), two at a time
+                const uint64_t sl2 = pack_f32x2(sl, sl), m2 = pack_f32x2(-m_use, -m_use);
+                uint64_t sum0 = 0, sum1 = 0;                     // two packed partial sums each
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float x[32], w[16];
                     tmem_ld32(s_row + 32 * c, x);
-                    if (edge) {
-                        const int left = prow - t0 - 32 * c;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = e <= left ? fmaf(x[e], sl, -m_use) : -INFINITY;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], sl, -m_use);
-                    }
+                    if (edge) mask_past(x, prow - t0 - 32 * c);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const uint32_t pw = pack_half2(fast_exp2(x[2 * e]), fast_exp2(x[2 * e + 1]));
-                        lt[e & 3] = add_f16_hi(add_f16_lo(lt[e & 3], pw), pw);
-                        w[e] = __uint_as_float(pw);
+                        float y0, y1;
+                        unpack_f32x2(fma_f32x2(pack_f32x2(x[2 * e], x[2 * e + 1]), sl2, m2), y0, y1);
+                        y0 = fast_exp2(y0);
+                        y1 = fast_exp2(y1);
+                        if (e & 1) sum1 = add_f32x2(sum1, pack_f32x2(y0, y1));
+                        else sum0 = add_f32x2(sum0, pack_f32x2(y0, y1));
+                        w[e] = __uint_as_float(pack_half2(y0, y1));
                     }
                     tmem_st16(s_row + 16 * c, w);                // P over logits already read
                     if (c & 1) {                                 // a half of P is in place (and O rescaled)
@@ -711,7 +736,11 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         mbar_arrive(p_full(t, c >> 1));
                     }
                 }
-                l_run += (lt[0] + lt[1]) + (lt[2] + lt[3]);
+                {
+                    float u0, u1;
+                    unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
+                    l_run += u0 + u1;
+                }
             }
             if (!ok) break;
             if (!(ok = wait_all(o_done(t), (cnt - 1) & 1))) break;

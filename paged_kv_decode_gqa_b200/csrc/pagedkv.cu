@@ -834,8 +834,8 @@ Int8Workspace int8_workspace(int sms) {
     const size_t slots = (size_t)sms * (kStreamWarps + 2);
     Int8Workspace w;
     w.tickets = 0;
-    // the larger of [levels][2 CTAs] (streaming) and [CTAs][2 streams][4 warps] (chunks)
-    w.ml = align256((size_t)sms * std::max(pkv::kTreeLevels * 2, 2 * 4) * sizeof(unsigned int));
+    // the larger of [levels][2 CTAs] (streaming) and [CTAs][2 streams][8 warps] (chunks)
+    w.ml = align256((size_t)sms * std::max(pkv::kTreeLevels * 2, 2 * 8) * sizeof(unsigned int));
     w.o = w.ml + align256(slots * 4 * sizeof(float4));
     w.stream_total = w.o + slots * 256 * sizeof(float4);
     w.parts = w.ml;
@@ -1533,8 +1533,9 @@ pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void
     prm.max_blocks_per_seq = max_blocks_per_seq;
     prm.num_blocks = num_blocks;
     prm.max_context_len = max_context_len;
-    prm.logit_scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
-    prm.key_sign = softmax_scale < 0.f ? -1.f : 1.f;
+    const float scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
+    prm.logit_scale_log2 = scale_log2 > 0.f ? scale_log2 : 1.f;
+    prm.key_sign = scale_log2 > 0.f ? (softmax_scale < 0.f ? -1.f : 1.f) : 0.f;
     return launch_chunk_int8(prm, q, k_cache, v_cache, kv_scales, workspace, workspace_bytes, st);
 }
 
