@@ -152,6 +152,45 @@ __device__ __forceinline__ void mask_past(float (&x)[32], int left) {
     for (int e = 0; e < 32; ++e) x[e] = e <= left ? x[e] : -INFINITY;
 }
 
+// The products of a KV tile, executed by the whole warp: one elected lane issues each. (Issued from a branch of
+// one lane, every operand is moved to the uniform registers one product at a time, through a queue that the
+// softmax keeps full: 100 to 250 cycles a product, where the product itself takes 72.)
+// D = A B^T over 128 channels: A and B K-major 128-byte-swizzled tiles of two 64-channel halves.
+__device__ __forceinline__ void umma_tile_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred e, z, o;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 z, 0, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+        "add.s64 a, %1, 0;\n\tadd.s64 b, %2, 0;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, z;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, o;\n\t"
+        "}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+}
+// D (+)= P V over 64 tokens: P in TMEM (two per column), V MN-major; `accumulate` 0 overwrites D.
+__device__ __forceinline__ void umma_half_ts(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, f, o;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 f, %4, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+        "add.s32 a, %1, 0;\n\tadd.s64 b, %2, 0;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, f;\n\t"
+        "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, o;\n\t"
+        "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, o;\n\t"
+        "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, o;\n\t"
+        "}"
+        :: "r"(d), "r"(p), "l"(v), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Arrives on `bar` when all products issued before (by the same elected lane) have completed.
+__device__ __forceinline__ void umma_commit_elected(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :: "r"(bar) : "memory");
+}
+
 // 16 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
     asm volatile(
@@ -559,20 +598,12 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         auto issue_s = [&](int t, int gg, int cnt, bool free_k, bool last) -> bool {
             if (cnt >= 1 && !wait_all(o_done(t), (cnt - 1) & 1)) return false;
             tc_fence_after();
-            if (lane == 0) {
-                const int s = gg & 1;
-                const uint32_t q = q_s(kNarrow ? 0 : t);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t koff = (kk >> 2) * S::kChunk + (kk & 3) * 32;
-                    umma_f16_ss(tmem_s(t), umma_desc_sw128(q + koff, 16, 1024), umma_desc_sw128(k_s(s) + koff, 16, 1024),
-                                kIdescS, kk > 0 ? 1u : 0u);
-                }
-                umma_commit(s_full(t));
-                if (free_k) umma_commit(k_empty(s));
-                if (last) umma_commit(q_empty);
-            }
-            __syncwarp();
+            const int s = gg & 1;
+            umma_tile_ss(tmem_s(t), umma_desc_sw128(q_s(kNarrow ? 0 : t), 16, 1024), umma_desc_sw128(k_s(s), 16, 1024),
+                         kIdescS);
+            umma_commit_elected(s_full(t));
+            if (free_k) umma_commit_elected(k_empty(s));
+            if (last) umma_commit_elected(q_empty);
             return true;
         };
         // O_t += P_t V(gg); `first`: the piece's first product on the stream overwrites O_t
@@ -582,19 +613,11 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int h = 0; h < 2; ++h) {                // as each half of P (64 tokens) comes in
                 if (!wait_all(p_full(t, h), cnt & 1)) return false;
                 tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_f16_ts(tmem_o(t), tmem_s(t) + 32 * h + 8 * kk,
-                                    umma_desc_sw128(v_s(s) + (4 * h + kk) * 2048, S::kChunk, 1024), kIdescPV,
-                                    (!first || h + kk > 0) ? 1u : 0u);
-                    if (h == 1) {
-                        umma_commit(o_done(t));
-                        if (free_v) umma_commit(v_empty(s));
-                    }
-                }
-                __syncwarp();
+                umma_half_ts(tmem_o(t), tmem_s(t) + 32 * h, umma_desc_sw128(v_s(s) + 8192 * h, S::kChunk, 1024), kIdescPV,
+                             first && h == 0 ? 0u : 1u);
             }
+            umma_commit_elected(o_done(t));
+            if (free_v) umma_commit_elected(v_empty(s));
             return true;
         };
         int gj = 0, k = 0;
@@ -647,7 +670,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             gj += n;
             ++k;
         }
-        if (lane == 0) umma_commit(drain);               // every product has completed before TMEM is freed
+        umma_commit_elected(drain);                      // every product has completed before TMEM is freed
         __syncwarp();
         mbar_wait(drain, 0);
     } else {
