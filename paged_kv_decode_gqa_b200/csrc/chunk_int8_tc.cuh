@@ -60,6 +60,14 @@ struct ChunkInt8Params {
     float key_sign;               // sign of softmax_scale (0 for 0), applied to the keys
 };
 
+#ifndef PKV_CONV_NARROW
+#define PKV_CONV_NARROW 8
+#endif
+#ifndef PKV_CONV_WIDE
+#define PKV_CONV_WIDE 4
+#endif
+constexpr int kConvNarrow = PKV_CONV_NARROW, kConvWide = PKV_CONV_WIDE;
+
 struct ChunkInt8Shape {
     static constexpr int kKvTok = 128;
     static constexpr int kChunk = 128 * 128;            // 64 channels of 128 rows, f16: 16 KiB
@@ -78,9 +86,9 @@ struct ChunkInt8Shape {
     static constexpr int kSmemBytes = kOffWords + 256;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one SM");
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kConvertWarp = 8;              // 8..11 K, 12..15 V
-    static constexpr int kTmaKWarp = 16, kTmaVWarp = 17, kMmaWarp = 18;
-    static constexpr int kThreads = 32 * 19;
+    static constexpr int kConvertWarp = 8;              // then the converters and three single warps
+    static constexpr int converters(bool narrow) { return narrow ? kConvNarrow : kConvWide; }
+    static constexpr int threads(bool narrow) { return 32 * (kConvertWarp + converters(narrow) + 3); }
     static constexpr uint32_t kTmemCols = 512;
     static constexpr float kRescaleThreshold = 8.f;
     static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
@@ -146,10 +154,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// 32 logits of consecutive tokens, those past number `left` hidden.
-__device__ __forceinline__ void mask_past(float (&x)[32], int left) {
+// Logits of consecutive tokens, those past number `left` hidden.
+template <int kCols>
+__device__ __forceinline__ void mask_past(float (&x)[kCols], int left) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = e <= left ? x[e] : -INFINITY;
+    for (int e = 0; e < kCols; ++e) x[e] = e <= left ? x[e] : -INFINITY;
 }
 
 // The products of a KV tile, executed by the whole warp: one elected lane issues each. (Issued from a branch of
@@ -205,12 +214,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
         : "memory");
 }
 
+// 32 or 64 TMEM columns of this thread's lane, in one round trip.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[64]) {
+    tmem_ld32x2(taddr, *reinterpret_cast<float (*)[32]>(&v[0]), taddr + 32, *reinterpret_cast<float (*)[32]>(&v[32]));
+}
+
 template <bool kNarrow>
-__global__ void __launch_bounds__(ChunkInt8Shape::kThreads, 1)
+__global__ void __launch_bounds__(ChunkInt8Shape::threads(kNarrow), 1)
 chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_s,
                   const ChunkInt8Params p) {
     using S = ChunkInt8Shape;
+    constexpr int kThreads = S::threads(kNarrow), kConverters = S::converters(kNarrow);
+    constexpr int kTmaKWarp = S::kConvertWarp + kConverters, kTmaVWarp = kTmaKWarp + 1, kMmaWarp = kTmaKWarp + 2;
+    constexpr int kCols = kConverters == 4 ? 64 : 32;    // logits a softmax thread holds (128 or 96 registers)
     constexpr int kRawStages = kNarrow ? 2 : 1;
     constexpr int kQTiles = kNarrow ? 1 : 2;             // query tiles of an item
     constexpr int kMinTiles = kNarrow ? 2 : 4;           // fewest KV tiles a CTA is given
@@ -259,7 +277,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         __syncthreads();
         int64_t before = 0;
         total = 0;
-        for (int i = 0; i < S::kThreads / 32; ++i) {
+        for (int i = 0; i < kThreads / 32; ++i) {
             before += i < warp ? s_red[i] : 0;
             total += s_red[i];
         }
@@ -271,7 +289,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     int ctas;
     {
         int64_t my_w = 0, my_incl = 0, first_total = 0;
-        for (int b0 = 0; b0 < p.batch; b0 += S::kThreads) {
+        for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
             const int b = b0 + (int)threadIdx.x;
             int64_t w = 0;
             if (b < p.batch) {
@@ -297,7 +315,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 s_first[1] = my_incl - my_w;
             }
             int64_t base = first_total;                  // more sequences than threads: scan again
-            for (int b0 = S::kThreads; b0 < p.batch && base <= u_lo; b0 += S::kThreads) {
+            for (int b0 = kThreads; b0 < p.batch && base <= u_lo; b0 += kThreads) {
                 const int b = b0 + (int)threadIdx.x;
                 const int64_t w = b < p.batch ? seq_tiles(b) * p.Hkv : 0;
                 int64_t total;
@@ -414,20 +432,20 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             mbar_init(v_full(t), 4);
             mbar_init(v_empty(t), 1);
             mbar_init(rk_full(t), 1);
-            mbar_init(rk_empty(t), 8);                   // the V warps read their scales there too
+            mbar_init(rk_empty(t), kConverters);         // (where V has its own warps, they read their scales there)
             mbar_init(rv_full(t), 1);
             mbar_init(rv_empty(t), 4);
         }
         mbar_init_fence();
     }
-    for (int i = threadIdx.x; i < kQTiles * (128 - rows) * 16; i += S::kThreads) {
+    for (int i = threadIdx.x; i < kQTiles * (128 - rows) * 16; i += kThreads) {
         const int t = i / ((128 - rows) * 16), k = i % ((128 - rows) * 16);
         const int r = rows + k / 16, part = k % 16;
         const uint32_t a = q_s(t) + (part >> 3) * S::kChunk + r * 128 + (part & 7) * 16;
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(a), "r"(0u) : "memory");
     }
     fence_proxy_async_shared();
-    if (warp == S::kMmaWarp) {
+    if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, S::kTmemCols);
         tmem_relinquish();
     }
@@ -457,9 +475,9 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     };
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
-    if (warp == S::kTmaKWarp || warp == S::kTmaVWarp) {
+    if (warp == kTmaKWarp || warp == kTmaVWarp) {
         // ================= TMA: codes of K (with Q and the scales), or of V =================
-        const bool is_k = warp == S::kTmaKWarp;
+        const bool is_k = warp == kTmaKWarp;
         const CUtensorMap* map = is_k ? &tm_k : &tm_v;
         if (lane == 0) {
             prefetch_tensormap(map);
@@ -519,9 +537,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // nothing of ours may be in flight when the CTA leaves
         for (int j = max(0, gj - kRawStages); j < gj; ++j) mbar_wait(full(j % kRawStages), (j / kRawStages) & 1);
         if (is_k && k >= 1) mbar_wait(q_full, (k - 1) & 1);
-    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + 8) {
-        // =============== codes of K (four warps) and of V (four) to f16 tiles: a token per thread ===============
-        const bool is_k = warp < S::kConvertWarp + 4;
+    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + kConverters) {
+        // ============ codes of K and of V to f16 tiles, a token per thread: four warps each, or four for both ============
         const int row = 32 * (warp & 3) + lane;                    // token of the KV tile
         const uint32_t sw = (uint32_t)(row & 7);
         // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`, 64 channels at
@@ -562,35 +579,62 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             if (live && !fine) flag_error(PKV_DEVERR_SCALE);
             return live && fine ? fminf(s, 511.75f) : 0.f;
         };
-        const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4) + (is_k ? 0u : 64u);
-        const float sign = is_k ? p.key_sign : 1.f;
-        auto tile_empty = [&](int d) { return is_k ? k_empty(d) : v_empty(d); };
+        const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4);
+        // stages the K (or V) of KV tile g, its j-th of the item, with this row's scale; false when a wait ran out
+        auto stage_tile = [&](bool is_k, int g, float scale) -> bool {
+            const int s = g % kRawStages, d = g & 1;
+            if (!is_k && !wait_all(rv_full(s), (g / kRawStages) & 1)) return false;
+            if (g >= 2 && !wait_all(is_k ? k_empty(d) : v_empty(d), ((g >> 1) - 1) & 1)) return false;
+            convert(is_k ? raw_k(s) : raw_v(s), is_k ? k_s(d) : v_s(d), scale);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(is_k ? rk_empty(s) : rv_empty(s));
+                mbar_arrive(is_k ? k_full(d) : v_full(d));
+            }
+            return true;
+        };
         Cursor cu = start;
         Piece pc;
-        int g = 0;                                                 // KV tiles so far
+        int gj = 0;                                                // KV tiles of earlier pieces
         bool ok = true;
         while (ok && next_piece(cu, pc)) {
-            for (int j = pc.j0; j < pc.j1; ++j, ++g) {
-                const int s = g % kRawStages, d = g & 1;
-                // (the scales come with the codes of K)
-                if (!(ok = wait_all(rk_full(s), (g / kRawStages) & 1))) break;
-                const float scale = row_scale(pc, j, raw_sc(s) + sc_off) * sign;
-                if (!is_k) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(rk_empty(s));
-                    if (!(ok = wait_all(rv_full(s), (g / kRawStages) & 1))) break;
+            const int n = pc.j1 - pc.j0;
+            if constexpr (kConverters == 8) {
+                const bool is_k = warp < S::kConvertWarp + 4;
+                for (int i = 0; i < n; ++i) {
+                    const int s = (gj + i) % kRawStages;
+                    // (the scales come with the codes of K)
+                    if (!(ok = wait_all(rk_full(s), ((gj + i) / kRawStages) & 1))) break;
+                    const float scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + (is_k ? 0u : 64u)) *
+                                        (is_k ? p.key_sign : 1.f);
+                    if (!is_k) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(rk_empty(s));
+                    }
+                    if (!(ok = stage_tile(is_k, gj + i, scale))) break;
                 }
-                if (g >= 2 && !(ok = wait_all(tile_empty(d), ((g >> 1) - 1) & 1))) break;
-                convert(is_k ? raw_k(s) : raw_v(s), is_k ? k_s(d) : v_s(d), scale);
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(is_k ? rk_empty(s) : rv_empty(s));
-                    mbar_arrive(is_k ? k_full(d) : v_full(d));
+            } else {
+                // K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
+                float v_scale = 0.f, v_next = 0.f;
+                for (int step = 0; step < 2 * n; ++step) {
+                    const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
+                    const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
+                    const int s = (gj + i) % kRawStages;
+                    float scale = v_scale;
+                    if (is_k) {
+                        if (!(ok = wait_all(rk_full(s), ((gj + i) / kRawStages) & 1))) break;
+                        scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
+                        v_next = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
+                        if (i == 0) v_scale = v_next;
+                    }
+                    if (!(ok = stage_tile(is_k, gj + i, scale))) break;
+                    if (!is_k) v_scale = v_next;
                 }
             }
+            gj += n;
         }
-    } else if (warp == S::kMmaWarp) {
+    } else if (warp == kMmaWarp) {
         // ===================================== MMA =====================================
         constexpr uint32_t kIdescS = umma_idesc_f16(128, 128, 0);    // Q K^T: both K-major
         constexpr uint32_t kIdescPV = umma_idesc_f16(128, 128, 1);   // P V: V is MN-major
@@ -705,15 +749,15 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tc_fence_after();
                 const int t0 = (pc.j0 + (kNarrow ? 2 * i + t : i)) * S::kKvTok;
                 const bool edge = t0 + S::kKvTok - 1 > first_pos;
-                // pass 1: the row's maximum, 32 columns at a time (loops, not unrolled code: see the conversion)
+                // pass 1: the row's maximum, kCols columns at a time (loops, not unrolled code: see the conversion)
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float x[32];
-                    tmem_ld32(s_row + 32 * c, x);
-                    if (edge) mask_past(x, prow - t0 - 32 * c);
+                for (int c = 0; c < 128; c += kCols) {
+                    float x[kCols];
+                    tmem_ld_cols(s_row + c, x);
+                    if (edge) mask_past(x, prow - t0 - c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
+                    for (int e = 0; e < kCols / 2; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
                 const bool raise = mt > m_run + S::kRescaleThreshold;
@@ -738,25 +782,29 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const uint64_t sl2 = pack_f32x2(sl, sl), m2 = pack_f32x2(-m_use, -m_use);
                 uint64_t sum0 = 0, sum1 = 0;                     // two packed partial sums each
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float x[32], w[16];
-                    tmem_ld32(s_row + 32 * c, x);
-                    if (edge) mask_past(x, prow - t0 - 32 * c);
+                for (int c = 0; c < 128; c += kCols) {
+                    float x[kCols];
+                    tmem_ld_cols(s_row + c, x);
+                    if (edge) mask_past(x, prow - t0 - c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float y0, y1;
-                        unpack_f32x2(fma_f32x2(pack_f32x2(x[2 * e], x[2 * e + 1]), sl2, m2), y0, y1);
-                        y0 = fast_exp2(y0);
-                        y1 = fast_exp2(y1);
-                        if (e & 1) sum1 = add_f32x2(sum1, pack_f32x2(y0, y1));
-                        else sum0 = add_f32x2(sum0, pack_f32x2(y0, y1));
-                        w[e] = __uint_as_float(pack_half2(y0, y1));
+                    for (int q = 0; q < kCols; q += 32) {
+                        float w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float y0, y1;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(x[q + 2 * e], x[q + 2 * e + 1]), sl2, m2), y0, y1);
+                            y0 = fast_exp2(y0);
+                            y1 = fast_exp2(y1);
+                            if (e & 1) sum1 = add_f32x2(sum1, pack_f32x2(y0, y1));
+                            else sum0 = add_f32x2(sum0, pack_f32x2(y0, y1));
+                            w[e] = __uint_as_float(pack_half2(y0, y1));
+                        }
+                        tmem_st16(s_row + (c + q) / 2, w);       // P over logits already read
                     }
-                    tmem_st16(s_row + 16 * c, w);                // P over logits already read
-                    if (c & 1) {                                 // a half of P is in place (and O rescaled)
+                    if ((c + kCols) % 64 == 0) {                 // a half of P is in place (and O rescaled)
                         tmem_wait_st();
                         tc_fence_before();
-                        mbar_arrive(p_full(t, c >> 1));
+                        mbar_arrive(p_full(t, c >> 6));
                     }
                 }
                 {
@@ -908,7 +956,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == S::kMmaWarp) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kTmemCols);
     }

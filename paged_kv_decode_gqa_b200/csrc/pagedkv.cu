@@ -889,7 +889,7 @@ cudaError_t launch_chunk(int sms, cudaStream_t st, const CUtensorMap& mq, const 
     static unsigned long long done = 0;
     const cudaError_t e = ensure_smem(kernel, S::kSmemBytes, &done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::kThreads), S::kSmemBytes, st, mq, mk, mv, ms, prm);
+    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::threads(kNarrow)), S::kSmemBytes, st, mq, mk, mv, ms, prm);
 }
 
 pkv_status launch_chunk_int8(pkv::ChunkInt8Params prm, const void* q, const void* k_cache, const void* v_cache,
