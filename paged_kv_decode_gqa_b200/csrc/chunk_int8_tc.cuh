@@ -51,7 +51,7 @@ struct ChunkInt8Params {
     const int32_t* context_lens;  // [B]
     const int32_t* query_start;   // [B + 1]
     uint8_t* parts;               // [2 * CTAs][2 streams][kPartBytes]
-    unsigned int* tickets;        // [CTAs][2][4], zero between calls
+    unsigned int* tickets;        // [CTAs], zero between calls
     int32_t batch, total, max_query_len;
     int32_t Hq, Hkv, G;
     int32_t max_blocks_per_seq, num_blocks, max_context_len;
@@ -59,14 +59,6 @@ struct ChunkInt8Params {
     float logit_scale_log2;       // |softmax_scale| * log2(e), or 1 when that is 0 (masked logits are -inf)
     float key_sign;               // sign of softmax_scale (0 for 0), applied to the keys
 };
-
-#ifndef PKV_CONV_NARROW
-#define PKV_CONV_NARROW 8
-#endif
-#ifndef PKV_CONV_WIDE
-#define PKV_CONV_WIDE 4
-#endif
-constexpr int kConvNarrow = PKV_CONV_NARROW, kConvWide = PKV_CONV_WIDE;
 
 struct ChunkInt8Shape {
     static constexpr int kKvTok = 128;
@@ -82,13 +74,13 @@ struct ChunkInt8Shape {
     static constexpr int kOffRaw = kOffV + 2 * kTile;
     static constexpr int kOffScales = kOffRaw + 2 * kRaw;
     static constexpr int kOffBars = kOffScales + 2 * kScales;
-    static constexpr int kOffWords = kOffBars + kBarBytes;   // block scan [20], first sequence [2], abort flag
+    static constexpr int kOffWords = kOffBars + kBarBytes;   // block scan [20], first sequence [2], abort flag, a barrier
     static constexpr int kSmemBytes = kOffWords + 256;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one SM");
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kConvertWarp = 8;              // then the converters and three single warps
-    static constexpr int converters(bool narrow) { return narrow ? kConvNarrow : kConvWide; }
-    static constexpr int threads(bool narrow) { return 32 * (kConvertWarp + converters(narrow) + 3); }
+    static constexpr int kConvertWarp = 8;              // 8..11 (eight converters leave the softmax 96 registers: slower)
+    static constexpr int kTmaKWarp = 12, kTmaVWarp = 13, kMmaWarp = 14;
+    static constexpr int kThreads = 32 * 15;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr float kRescaleThreshold = 8.f;
     static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
@@ -128,6 +120,12 @@ __device__ __forceinline__ void dequant4(uint32_t w, const RowScale& s, uint32_t
 __device__ __forceinline__ uint32_t times(uint32_t a, __half2 f) {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Untiled bulk copy global -> shared of a multiple of 16 bytes, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 // Packed fp32 pairs: one instruction for two lanes of arithmetic.
@@ -221,14 +219,12 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[64]) {
 }
 
 template <bool kNarrow>
-__global__ void __launch_bounds__(ChunkInt8Shape::threads(kNarrow), 1)
+__global__ void __launch_bounds__(ChunkInt8Shape::kThreads, 1)
 chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_s,
                   const ChunkInt8Params p) {
     using S = ChunkInt8Shape;
-    constexpr int kThreads = S::threads(kNarrow), kConverters = S::converters(kNarrow);
-    constexpr int kTmaKWarp = S::kConvertWarp + kConverters, kTmaVWarp = kTmaKWarp + 1, kMmaWarp = kTmaKWarp + 2;
-    constexpr int kCols = kConverters == 4 ? 64 : 32;    // logits a softmax thread holds (128 or 96 registers)
+    constexpr int kCols = 64;                            // logits a softmax thread holds
     constexpr int kRawStages = kNarrow ? 2 : 1;
     constexpr int kQTiles = kNarrow ? 1 : 2;             // query tiles of an item
     constexpr int kMinTiles = kNarrow ? 2 : 4;           // fewest KV tiles a CTA is given
@@ -277,7 +273,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         __syncthreads();
         int64_t before = 0;
         total = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
+        for (int i = 0; i < S::kThreads / 32; ++i) {
             before += i < warp ? s_red[i] : 0;
             total += s_red[i];
         }
@@ -289,7 +285,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     int ctas;
     {
         int64_t my_w = 0, my_incl = 0, first_total = 0;
-        for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+        for (int b0 = 0; b0 < p.batch; b0 += S::kThreads) {
             const int b = b0 + (int)threadIdx.x;
             int64_t w = 0;
             if (b < p.batch) {
@@ -315,7 +311,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 s_first[1] = my_incl - my_w;
             }
             int64_t base = first_total;                  // more sequences than threads: scan again
-            for (int b0 = kThreads; b0 < p.batch && base <= u_lo; b0 += kThreads) {
+            for (int b0 = S::kThreads; b0 < p.batch && base <= u_lo; b0 += S::kThreads) {
                 const int b = b0 + (int)threadIdx.x;
                 const int64_t w = b < p.batch ? seq_tiles(b) * p.Hkv : 0;
                 int64_t total;
@@ -356,6 +352,11 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             ++start.q;
         }
     }
+    // where CTA c keeps its piece of an item (stream t): slot 0 if the piece starts the CTA's run, as it does in every
+    // CTA behind the item's first one, else slot 1 (the CTA's last piece)
+    auto part_of = [&](int c, int slot, int t) -> uint8_t* {
+        return p.parts + ((int64_t)(2 * c + slot) * 2 + t) * S::kPartBytes;
+    };
     auto next_piece = [&](Cursor& cu, Piece& pc) -> bool {
         while (cu.u < u_hi && cu.b < p.batch) {
             int qs0, n, L;
@@ -413,11 +414,13 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // narrow: the odd stream's (m, l) of a piece are in TMEM; the even stream has read them
     const uint32_t x_full = bars + 216, x_read = bars + 224;
     const uint32_t tmem_slot = bars + 248;
+    const uint32_t merge_bar = base + S::kOffWords + 192;
     const int rows = G * T;                              // rows of Q the TMA fills; the rest stay zero
     if (threadIdx.x == 0) {
         *s_abort = 0;
         mbar_init(x_full, 128);
         mbar_init(x_read, 128);
+        mbar_init(merge_bar, 1);
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(drain, 1);
@@ -432,20 +435,20 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             mbar_init(v_full(t), 4);
             mbar_init(v_empty(t), 1);
             mbar_init(rk_full(t), 1);
-            mbar_init(rk_empty(t), kConverters);         // (where V has its own warps, they read their scales there)
+            mbar_init(rk_empty(t), 4);
             mbar_init(rv_full(t), 1);
             mbar_init(rv_empty(t), 4);
         }
         mbar_init_fence();
     }
-    for (int i = threadIdx.x; i < kQTiles * (128 - rows) * 16; i += kThreads) {
+    for (int i = threadIdx.x; i < kQTiles * (128 - rows) * 16; i += S::kThreads) {
         const int t = i / ((128 - rows) * 16), k = i % ((128 - rows) * 16);
         const int r = rows + k / 16, part = k % 16;
         const uint32_t a = q_s(t) + (part >> 3) * S::kChunk + r * 128 + (part & 7) * 16;
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(a), "r"(0u) : "memory");
     }
     fence_proxy_async_shared();
-    if (warp == kMmaWarp) {
+    if (warp == S::kMmaWarp) {
         tmem_alloc(tmem_slot, S::kTmemCols);
         tmem_relinquish();
     }
@@ -475,9 +478,9 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     };
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
-    if (warp == kTmaKWarp || warp == kTmaVWarp) {
+    if (warp == S::kTmaKWarp || warp == S::kTmaVWarp) {
         // ================= TMA: codes of K (with Q and the scales), or of V =================
-        const bool is_k = warp == kTmaKWarp;
+        const bool is_k = warp == S::kTmaKWarp;
         const CUtensorMap* map = is_k ? &tm_k : &tm_v;
         if (lane == 0) {
             prefetch_tensormap(map);
@@ -537,8 +540,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // nothing of ours may be in flight when the CTA leaves
         for (int j = max(0, gj - kRawStages); j < gj; ++j) mbar_wait(full(j % kRawStages), (j / kRawStages) & 1);
         if (is_k && k >= 1) mbar_wait(q_full, (k - 1) & 1);
-    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + kConverters) {
-        // ============ codes of K and of V to f16 tiles, a token per thread: four warps each, or four for both ============
+    } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + 4) {
+        // ========================= codes to f16 tiles: a token per thread =========================
         const int row = 32 * (warp & 3) + lane;                    // token of the KV tile
         const uint32_t sw = (uint32_t)(row & 7);
         // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`, 64 channels at
@@ -600,41 +603,25 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bool ok = true;
         while (ok && next_piece(cu, pc)) {
             const int n = pc.j1 - pc.j0;
-            if constexpr (kConverters == 8) {
-                const bool is_k = warp < S::kConvertWarp + 4;
-                for (int i = 0; i < n; ++i) {
-                    const int s = (gj + i) % kRawStages;
-                    // (the scales come with the codes of K)
+            // K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
+            float v_scale = 0.f, v_next = 0.f;
+            for (int step = 0; step < 2 * n; ++step) {
+                const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
+                const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
+                const int s = (gj + i) % kRawStages;
+                float scale = v_scale;
+                if (is_k) {
                     if (!(ok = wait_all(rk_full(s), ((gj + i) / kRawStages) & 1))) break;
-                    const float scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + (is_k ? 0u : 64u)) *
-                                        (is_k ? p.key_sign : 1.f);
-                    if (!is_k) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(rk_empty(s));
-                    }
-                    if (!(ok = stage_tile(is_k, gj + i, scale))) break;
+                    scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
+                    v_next = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
+                    if (i == 0) v_scale = v_next;
                 }
-            } else {
-                // K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
-                float v_scale = 0.f, v_next = 0.f;
-                for (int step = 0; step < 2 * n; ++step) {
-                    const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
-                    const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
-                    const int s = (gj + i) % kRawStages;
-                    float scale = v_scale;
-                    if (is_k) {
-                        if (!(ok = wait_all(rk_full(s), ((gj + i) / kRawStages) & 1))) break;
-                        scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
-                        v_next = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
-                        if (i == 0) v_scale = v_next;
-                    }
-                    if (!(ok = stage_tile(is_k, gj + i, scale))) break;
-                    if (!is_k) v_scale = v_next;
-                }
+                if (!(ok = stage_tile(is_k, gj + i, scale))) break;
+                if (!is_k) v_scale = v_next;
             }
             gj += n;
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == S::kMmaWarp) {
         // ===================================== MMA =====================================
         constexpr uint32_t kIdescS = umma_idesc_f16(128, 128, 0);    // Q K^T: both K-major
         constexpr uint32_t kIdescPV = umma_idesc_f16(128, 128, 1);   // P V: V is MN-major
@@ -888,77 +875,142 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 release_o();
                 continue;
             }
-            // ---- a piece of an item cut at a CTA boundary: store (m, l, O), take a ticket for the
-            // warp's 32 rows; the last one merges out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k ----
-            const int c_first = cta_of(pc.u), c_last = cta_of(pc.u + pc.ntiles - 1);
-            auto part_of = [&](int c) -> uint8_t* {              // slot 0: the piece starts CTA c's run, else 1
-                const int slot = 2 * c + (max(pc.u, range_lo(c)) == range_lo(c) ? 0 : 1);
-                return p.parts + ((int64_t)slot * 2 + t) * S::kPartBytes;
-            };
-            {
-                uint8_t* part = part_of((int)blockIdx.x);
-                float4* po = reinterpret_cast<float4*>(part);
+            // ---- a piece of an item cut at a CTA boundary leaves (m, l, O) for the merge at the CTA's end ----
+            uint8_t* part = part_of((int)blockIdx.x, pc.u <= u_lo ? 0 : 1, t);
+            float4* po = reinterpret_cast<float4*>(part);        // [32 float4 of channels][lp rows]
+            const int lp = (min(T, pc.nq - (kNarrow ? 0 : t * T)) * G + 7) & ~7;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float o[32];
-                    load_o(c, o);
-                    if (valid) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            __stcg(po + (8 * c + q) * 128 + r, make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
-                    }
-                }
-                if (valid) __stcg(reinterpret_cast<float2*>(part + 128 * 128 * 4) + r, make_float2(m_run, l_run));
-            }
-            release_o();
-            // the warp barrier orders every lane's stores before lane 0's release-acquire ticket; the
-            // merger's loads follow its acquire
-            __syncwarp();
-            unsigned int* tick = p.tickets + ((int64_t)c_last * 2 + t) * 4 + quarter;
-            unsigned int prev = 0;
-            if (lane == 0) prev = atomic_add_acq_rel_gpu(tick, 1u);
-            prev = __shfl_sync(0xffffffffu, prev, 0);
-            __syncwarp();
-            if (prev != (unsigned int)(c_last - c_first)) continue;   // another piece's warp merges
-            if (lane == 0) *tick = 0u;                           // ready for the next call
-            if (!valid) continue;
-            // in the order of the pieces, whoever merges: the result does not depend on timing
-            auto ml_of = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part_of(c) + 128 * 128 * 4) + r); };
-            float M = kLogitFloor, den = 0.f;
-#pragma unroll 1
-            for (int c = c_first; c <= c_last; ++c) M = fmaxf(M, ml_of(c).x);
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {                        // 32 channels at a time
+            for (int c = 0; c < 4; ++c) {
                 float o[32];
+                load_o(c, o);
+                if (valid) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                den = 0.f;
-#pragma unroll 1
-                for (int c = c_first; c <= c_last; ++c) {
-                    const float4* src = reinterpret_cast<const float4*>(part_of(c)) + 8 * h * 128 + r;
-                    float4 v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = __ldcg(src + q * 128);
-                    const float2 ml = ml_of(c);
-                    const float w = fast_exp2(ml.x - M);         // 0 for a piece that saw no position of the row
-                    den = fmaf(w, ml.y, den);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        o[4 * q] = fmaf(w, v[q].x, o[4 * q]);
-                        o[4 * q + 1] = fmaf(w, v[q].y, o[4 * q + 1]);
-                        o[4 * q + 2] = fmaf(w, v[q].z, o[4 * q + 2]);
-                        o[4 * q + 3] = fmaf(w, v[q].w, o[4 * q + 3]);
-                    }
+                    for (int q = 0; q < 8; ++q)
+                        __stcg(po + (8 * c + q) * lp + r, make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
                 }
-                store_out(h, o, 1.f / den);
             }
+            if (valid) __stcg(reinterpret_cast<float2*>(part + 128 * 128 * 4) + r, make_float2(m_run, l_run));
+            release_o();
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == S::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kTmemCols);
+    }
+    if (*s_abort) return;                                // (uniform: the barrier lies between it and the last write)
+
+    // ---- the items this CTA has a piece of (its first and its last one, at most): the CTA that takes an item's
+    // last ticket merges its pieces, all threads together, through the shared memory that is free by now, three
+    // pieces at a time by bulk copy. (Merged by each warp as soon as a piece was done, the loads came eight at a
+    // time in one chain: 4 tokens on one 2000-token context took 28 us.) The block's barrier orders the pieces'
+    // stores before the release-acquire ticket; the copies behind its acquire come after the next barrier. ----
+    Piece cut0{}, cut1{};
+    int n_cut = 0;
+    {
+        Cursor cu = start;
+        Piece pc;
+        while (next_piece(cu, pc)) {
+            if (pc.j0 == 0 && pc.j1 == pc.ntiles) continue;
+            if (n_cut == 0) cut0 = pc;
+            else cut1 = pc;
+            ++n_cut;
+        }
+    }
+    if (n_cut == 0) return;
+    if (warp < n_cut && lane == 0) {                             // an item is known by the last CTA it reaches
+        const Piece& pc = warp ? cut1 : cut0;
+        const int c_last = cta_of(pc.u + pc.ntiles - 1);
+        const bool last = atomic_add_acq_rel_gpu(p.tickets + c_last, 1u) == (unsigned int)(c_last - cta_of(pc.u));
+        if (last) p.tickets[c_last] = 0u;                        // ready for the next call
+        s_first[warp] = last ? 1 : 0;
+    }
+    __syncthreads();
+    const bool won0 = s_first[0] != 0, won1 = n_cut > 1 && s_first[1] != 0;
+    float* weight = reinterpret_cast<float*>(smem_raw + S::kOffScales);      // [slot][row], then 1 / sum
+    uint32_t phase = 0;
+#pragma unroll 1
+    for (int kt = 0; kt < 2 * kQTiles; ++kt) {                   // (item, query tile)
+        const int k = kt / kQTiles, t = kt - k * kQTiles;
+        if (!(k ? won1 : won0)) continue;
+        const int64_t u_item = k ? cut1.u : cut0.u;
+        const int row_first = (k ? cut1.row0 : cut0.row0) + t * T, head0 = (k ? cut1.g : cut0.g) * G;
+        const int live = min(T, (k ? cut1.nq : cut0.nq) - t * T) * G;        // rows of the tile
+        if (live <= 0) continue;
+        const int lp = (live + 7) & ~7;
+        const int c_first = cta_of(u_item), c_last = cta_of(u_item + (k ? cut1.ntiles : cut0.ntiles) - 1);
+        const int first_slot = u_item <= range_lo(c_first) ? 0 : 1;
+        float M = kLogitFloor, den = 0.f;                        // of row threadIdx.x, over the pieces so far
+        // (the order of the pieces decides the result, not who merges)
+        for (int c0 = c_first; c0 <= c_last;) {
+            // a running result sits in slot 0 after the first round
+            const int s0 = c0 == c_first ? 0 : 1, n_new = min(3 - s0, c_last - c0 + 1), n_all = s0 + n_new;
+            auto piece_at = [&](int u) { return part_of(c0 + u, c0 + u == c_first ? first_slot : 0, t); };
+            if (threadIdx.x == 0) {
+                fence_proxy_async_shared();
+                mbar_arrive_expect_tx(merge_bar, (uint32_t)(n_new * 512 * lp));
+                for (int u = 0; u < n_new; ++u)
+                    bulk_load(base + (uint32_t)(s0 + u) * 65536u, piece_at(u), (uint32_t)(512 * lp), merge_bar);
+            }
+            if ((int)threadIdx.x < live) {
+                float m_new = M;
+                float2 ml[3];
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                    ml[u] = make_float2(-INFINITY, 0.f);         // (as is a piece that saw no position of the row)
+                    if (u < n_new) ml[u] = __ldcg(reinterpret_cast<const float2*>(piece_at(u) + 128 * 128 * 4) + threadIdx.x);
+                    m_new = fmaxf(m_new, ml[u].x);
+                }
+                const float a = fast_exp2(M - m_new);
+                den *= a;
+                if (s0) weight[threadIdx.x] = a;
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                    const float w = fast_exp2(ml[u].x - m_new);
+                    den = fmaf(w, ml[u].y, den);
+                    if (u < n_new) weight[128 * (s0 + u) + threadIdx.x] = w;
+                }
+                weight[128 * 3 + threadIdx.x] = 1.f / den;
+                M = m_new;
+            }
+            // all leave together when the copies do not come
+            if (__syncthreads_or(!mbar_wait(merge_bar, phase))) return;
+            phase ^= 1;
+            c0 += n_new;
+            const bool done = c0 > c_last;
+            // lane: row r = 8 i + lane % 8, float4 of channels q = 4 j + lane / 8
+            const int q_lane = lane >> 3, r_lane = lane & 7;
+#pragma unroll 4
+            for (int blk = warp; blk < lp; blk += S::kThreads / 32) {        // lp / 8 row groups x 8 channel groups
+                const int r = 8 * (blk >> 3) + r_lane, q = 4 * (blk & 7) + q_lane;
+                const float4* at = reinterpret_cast<const float4*>(smem_raw) + q * lp + r;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < live) {
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        if (u < n_all) {
+                            const float4 v = at[4096 * u];
+                            const float w = weight[128 * u + r];
+                            acc.x = fmaf(w, v.x, acc.x);
+                            acc.y = fmaf(w, v.y, acc.y);
+                            acc.z = fmaf(w, v.z, acc.z);
+                            acc.w = fmaf(w, v.w, acc.w);
+                        }
+                    }
+                    if (!done) {
+                        const_cast<float4*>(at)[0] = acc;
+                    } else {
+                        const float inv = weight[128 * 3 + r];
+                        const int ti = r / G;
+                        __half* dst = p.out + ((int64_t)(row_first + ti) * p.Hq + head0 + r - ti * G) * kHeadDim;
+                        reinterpret_cast<uint2*>(dst)[q] = make_uint2(pack_half2(acc.x * inv, acc.y * inv),
+                                                                      pack_half2(acc.z * inv, acc.w * inv));
+                    }
+                }
+            }
+            __syncthreads();                                     // the slots and weights may be overwritten
+        }
     }
 }
 

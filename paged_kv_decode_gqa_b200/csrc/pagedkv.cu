@@ -834,8 +834,8 @@ Int8Workspace int8_workspace(int sms) {
     const size_t slots = (size_t)sms * (kStreamWarps + 2);
     Int8Workspace w;
     w.tickets = 0;
-    // the larger of [levels][2 CTAs] (streaming) and [CTAs][2 streams][8 warps] (chunks)
-    w.ml = align256((size_t)sms * std::max(pkv::kTreeLevels * 2, 2 * 8) * sizeof(unsigned int));
+    // [levels][2 CTAs] (streaming), [CTAs] (chunks)
+    w.ml = align256((size_t)sms * pkv::kTreeLevels * 2 * sizeof(unsigned int));
     w.o = w.ml + align256(slots * 4 * sizeof(float4));
     w.stream_total = w.o + slots * 256 * sizeof(float4);
     w.parts = w.ml;
@@ -889,7 +889,7 @@ cudaError_t launch_chunk(int sms, cudaStream_t st, const CUtensorMap& mq, const 
     static unsigned long long done = 0;
     const cudaError_t e = ensure_smem(kernel, S::kSmemBytes, &done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::threads(kNarrow)), S::kSmemBytes, st, mq, mk, mv, ms, prm);
+    return launch_pdl(kernel, dim3((unsigned)sms), dim3(S::kThreads), S::kSmemBytes, st, mq, mk, mv, ms, prm);
 }
 
 pkv_status launch_chunk_int8(pkv::ChunkInt8Params prm, const void* q, const void* k_cache, const void* v_cache,
