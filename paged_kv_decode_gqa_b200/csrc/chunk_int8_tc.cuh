@@ -51,7 +51,7 @@ struct ChunkInt8Params {
     const int32_t* context_lens;  // [B]
     const int32_t* query_start;   // [B + 1]
     uint8_t* parts;               // [2 * CTAs][2 streams][kPartBytes]
-    unsigned int* tickets;        // [CTAs], zero between calls
+    unsigned int* tickets;        // [CTAs] (narrow) or [CTAs][2 streams][4 warps], zero between calls
     int32_t batch, total, max_query_len;
     int32_t Hq, Hkv, G;
     int32_t max_blocks_per_seq, num_blocks, max_context_len;
@@ -239,6 +239,10 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     long long* s_red = reinterpret_cast<long long*>(smem_raw + S::kOffWords);     // [20]
     long long* s_first = s_red + 20;                                              // [2]
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_first + 2);
+    // the items this CTA holds a piece of, as the softmax meets them
+    struct CutItem { long long u; int row0, nq, g, ntiles; };
+    CutItem* s_cut = reinterpret_cast<CutItem*>(smem_raw + S::kOffWords + 200);   // [2]
+    int* s_cuts = reinterpret_cast<int*>(smem_raw + S::kOffWords + 248);          // how many
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.G, T = p.tokens;
     const int per_item = kQTiles * T;                    // query tokens of an item
@@ -418,6 +422,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int rows = G * T;                              // rows of Q the TMA fills; the rest stay zero
     if (threadIdx.x == 0) {
         *s_abort = 0;
+        *s_cuts = 0;
         mbar_init(x_full, 128);
         mbar_init(x_read, 128);
         mbar_init(merge_bar, 1);
@@ -875,7 +880,16 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 release_o();
                 continue;
             }
-            // ---- a piece of an item cut at a CTA boundary leaves (m, l, O) for the merge at the CTA's end ----
+            if (kNarrow && threadIdx.x == 0) {
+                CutItem& it = s_cut[*s_cuts];
+                it.u = pc.u;
+                it.row0 = pc.row0;
+                it.nq = pc.nq;
+                it.g = pc.g;
+                it.ntiles = pc.ntiles;
+                ++*s_cuts;
+            }
+            // ---- a piece of an item cut at a CTA boundary: its (m, l, O) go to the workspace ----
             uint8_t* part = part_of((int)blockIdx.x, pc.u <= u_lo ? 0 : 1, t);
             float4* po = reinterpret_cast<float4*>(part);        // [32 float4 of channels][lp rows]
             const int lp = (min(T, pc.nq - (kNarrow ? 0 : t * T)) * G + 7) & ~7;
@@ -891,6 +905,52 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             if (valid) __stcg(reinterpret_cast<float2*>(part + 128 * 128 * 4) + r, make_float2(m_run, l_run));
             release_o();
+            if constexpr (kNarrow) continue;                     // merged at the CTA's end
+            // Wide: the warp's ticket for its 32 rows. The warp barrier orders every lane's stores before lane
+            // 0's release-acquire; the loads of the last one, which merges, follow its acquire:
+            // out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of the pieces, whoever merges.
+            // The other warps go on meanwhile. (Merged at the CTA's end as below, 512 tokens on 8 x 2048
+            // contexts took 171 us instead of 162; narrow chunks have few rows, hence few warps, for this.)
+            __syncwarp();
+            const int c_first = cta_of(pc.u), c_last = cta_of(pc.u + pc.ntiles - 1);
+            unsigned int* tick = p.tickets + ((int64_t)c_last * 2 + t) * 4 + quarter;
+            unsigned int prev = 0;
+            if (lane == 0) prev = atomic_add_acq_rel_gpu(tick, 1u);
+            prev = __shfl_sync(0xffffffffu, prev, 0);
+            __syncwarp();
+            if (prev != (unsigned int)(c_last - c_first)) continue;
+            if (lane == 0) *tick = 0u;                           // ready for the next call
+            if (!valid) continue;
+            const int first_slot = pc.u <= range_lo(c_first) ? 0 : 1;
+            auto piece_at = [&](int c) { return part_of(c, c == c_first ? first_slot : 0, t); };
+            auto ml_of = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(piece_at(c) + 128 * 128 * 4) + r); };
+            float M = kLogitFloor;
+#pragma unroll 1
+            for (int c = c_first; c <= c_last; ++c) M = fmaxf(M, ml_of(c).x);
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {                        // 32 channels at a time
+                float o[32], den = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 1
+                for (int c = c_first; c <= c_last; ++c) {
+                    const float4* src = reinterpret_cast<const float4*>(piece_at(c)) + 8 * h * lp + r;
+                    float4 v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = __ldcg(src + q * lp);
+                    const float2 ml = ml_of(c);
+                    const float w = fast_exp2(ml.x - M);         // 0 for a piece that saw no position of the row
+                    den = fmaf(w, ml.y, den);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        o[4 * q] = fmaf(w, v[q].x, o[4 * q]);
+                        o[4 * q + 1] = fmaf(w, v[q].y, o[4 * q + 1]);
+                        o[4 * q + 2] = fmaf(w, v[q].z, o[4 * q + 2]);
+                        o[4 * q + 3] = fmaf(w, v[q].w, o[4 * q + 3]);
+                    }
+                }
+                store_out(h, o, 1.f / den);
+            }
         }
     }
     tc_fence_before();
@@ -899,54 +959,45 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_after();
         tmem_dealloc(tmem, S::kTmemCols);
     }
-    if (*s_abort) return;                                // (uniform: the barrier lies between it and the last write)
+    if (!kNarrow || *s_abort) return;                    // (uniform: the barrier lies between it and the last write)
 
-    // ---- the items this CTA has a piece of (its first and its last one, at most): the CTA that takes an item's
-    // last ticket merges its pieces, all threads together, through the shared memory that is free by now, three
-    // pieces at a time by bulk copy. (Merged by each warp as soon as a piece was done, the loads came eight at a
-    // time in one chain: 4 tokens on one 2000-token context took 28 us.) The block's barrier orders the pieces'
-    // stores before the release-acquire ticket; the copies behind its acquire come after the next barrier. ----
-    Piece cut0{}, cut1{};
-    int n_cut = 0;
-    {
-        Cursor cu = start;
-        Piece pc;
-        while (next_piece(cu, pc)) {
-            if (pc.j0 == 0 && pc.j1 == pc.ntiles) continue;
-            if (n_cut == 0) cut0 = pc;
-            else cut1 = pc;
-            ++n_cut;
-        }
-    }
+    // ---- narrow: the items this CTA has a piece of (its first and its last one, at most). The CTA that takes an
+    // item's last ticket merges its pieces, all threads together, through the shared memory that is free by now,
+    // three pieces at a time by bulk copy. (Merged warp by warp as above, 4 tokens on one 2000-token context took
+    // 28 us instead of 18.) The block's barrier orders the pieces' stores before the release-acquire ticket; the
+    // copies behind its acquire come after the next barrier. ----
+    const int n_cut = *s_cuts;
     if (n_cut == 0) return;
     if (warp < n_cut && lane == 0) {                             // an item is known by the last CTA it reaches
-        const Piece& pc = warp ? cut1 : cut0;
-        const int c_last = cta_of(pc.u + pc.ntiles - 1);
-        const bool last = atomic_add_acq_rel_gpu(p.tickets + c_last, 1u) == (unsigned int)(c_last - cta_of(pc.u));
+        const CutItem& it = s_cut[warp];
+        const int c_last = cta_of(it.u + it.ntiles - 1), others = c_last - cta_of(it.u);
+        const bool last = atomic_add_acq_rel_gpu(p.tickets + c_last, 1u) == (unsigned int)others;
         if (last) p.tickets[c_last] = 0u;                        // ready for the next call
         s_first[warp] = last ? 1 : 0;
     }
     __syncthreads();
     const bool won0 = s_first[0] != 0, won1 = n_cut > 1 && s_first[1] != 0;
     float* weight = reinterpret_cast<float*>(smem_raw + S::kOffScales);      // [slot][row], then 1 / sum
+    long long* out_of_row = reinterpret_cast<long long*>(smem_raw + 3 * 65536);             // behind the three slots
     uint32_t phase = 0;
 #pragma unroll 1
-    for (int kt = 0; kt < 2 * kQTiles; ++kt) {                   // (item, query tile)
-        const int k = kt / kQTiles, t = kt - k * kQTiles;
+    for (int k = 0; k < n_cut; ++k) {
         if (!(k ? won1 : won0)) continue;
-        const int64_t u_item = k ? cut1.u : cut0.u;
-        const int row_first = (k ? cut1.row0 : cut0.row0) + t * T, head0 = (k ? cut1.g : cut0.g) * G;
-        const int live = min(T, (k ? cut1.nq : cut0.nq) - t * T) * G;        // rows of the tile
-        if (live <= 0) continue;
+        const CutItem it = s_cut[k];
+        const int live = it.nq * G;                              // rows
         const int lp = (live + 7) & ~7;
-        const int c_first = cta_of(u_item), c_last = cta_of(u_item + (k ? cut1.ntiles : cut0.ntiles) - 1);
-        const int first_slot = u_item <= range_lo(c_first) ? 0 : 1;
+        const int c_first = cta_of(it.u), c_last = cta_of(it.u + it.ntiles - 1);
+        const int first_slot = it.u <= range_lo(c_first) ? 0 : 1;
+        if ((int)threadIdx.x < live) {                           // where row threadIdx.x goes
+            const int ti = threadIdx.x / G;
+            out_of_row[threadIdx.x] = ((long long)(it.row0 + ti) * p.Hq + it.g * G + threadIdx.x - ti * G) * kHeadDim;
+        }
         float M = kLogitFloor, den = 0.f;                        // of row threadIdx.x, over the pieces so far
         // (the order of the pieces decides the result, not who merges)
         for (int c0 = c_first; c0 <= c_last;) {
             // a running result sits in slot 0 after the first round
             const int s0 = c0 == c_first ? 0 : 1, n_new = min(3 - s0, c_last - c0 + 1), n_all = s0 + n_new;
-            auto piece_at = [&](int u) { return part_of(c0 + u, c0 + u == c_first ? first_slot : 0, t); };
+            auto piece_at = [&](int u) { return part_of(c0 + u, c0 + u == c_first ? first_slot : 0, 0); };
             if (threadIdx.x == 0) {
                 fence_proxy_async_shared();
                 mbar_arrive_expect_tx(merge_bar, (uint32_t)(n_new * 512 * lp));
@@ -979,34 +1030,42 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             phase ^= 1;
             c0 += n_new;
             const bool done = c0 > c_last;
-            // lane: row r = 8 i + lane % 8, float4 of channels q = 4 j + lane / 8
+            // a warp takes eight rows x four float4 of channels at a time (whole 32-byte sectors of the output)
             const int q_lane = lane >> 3, r_lane = lane & 7;
-#pragma unroll 4
-            for (int blk = warp; blk < lp; blk += S::kThreads / 32) {        // lp / 8 row groups x 8 channel groups
-                const int r = 8 * (blk >> 3) + r_lane, q = 4 * (blk & 7) + q_lane;
-                const float4* at = reinterpret_cast<const float4*>(smem_raw) + q * lp + r;
+            const float4* slot = reinterpret_cast<const float4*>(smem_raw);
+            auto combine = [&](int blk, int& r, int& q) -> float4 {
+                r = 8 * (blk >> 3) + r_lane;
+                q = 4 * (blk & 7) + q_lane;
+                const int at = q * lp + r;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < live) {
 #pragma unroll
-                    for (int u = 0; u < 3; ++u) {
-                        if (u < n_all) {
-                            const float4 v = at[4096 * u];
-                            const float w = weight[128 * u + r];
-                            acc.x = fmaf(w, v.x, acc.x);
-                            acc.y = fmaf(w, v.y, acc.y);
-                            acc.z = fmaf(w, v.z, acc.z);
-                            acc.w = fmaf(w, v.w, acc.w);
-                        }
+                for (int u = 0; u < 3; ++u) {
+                    if (u < n_all) {
+                        const float4 v = slot[4096 * u + at];
+                        const float w = weight[128 * u + r];
+                        acc.x = fmaf(w, v.x, acc.x);
+                        acc.y = fmaf(w, v.y, acc.y);
+                        acc.z = fmaf(w, v.z, acc.z);
+                        acc.w = fmaf(w, v.w, acc.w);
                     }
-                    if (!done) {
-                        const_cast<float4*>(at)[0] = acc;
-                    } else {
-                        const float inv = weight[128 * 3 + r];
-                        const int ti = r / G;
-                        __half* dst = p.out + ((int64_t)(row_first + ti) * p.Hq + head0 + r - ti * G) * kHeadDim;
-                        reinterpret_cast<uint2*>(dst)[q] = make_uint2(pack_half2(acc.x * inv, acc.y * inv),
-                                                                      pack_half2(acc.z * inv, acc.w * inv));
-                    }
+                }
+                return acc;
+            };
+            if (done) {
+#pragma unroll 2
+                for (int blk = warp; blk < lp; blk += S::kThreads / 32) {
+                    int r, q;
+                    const float4 acc = combine(blk, r, q);
+                    const float inv = weight[128 * 3 + r];
+                    if (r < live)
+                        reinterpret_cast<uint2*>(p.out + out_of_row[r])[q] =
+                            make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
+                }
+            } else {
+                for (int blk = warp; blk < lp; blk += S::kThreads / 32) {
+                    int r, q;
+                    const float4 acc = combine(blk, r, q);
+                    reinterpret_cast<float4*>(smem_raw)[q * lp + r] = acc;
                 }
             }
             __syncthreads();                                     // the slots and weights may be overwritten

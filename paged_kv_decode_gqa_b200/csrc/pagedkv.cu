@@ -834,8 +834,8 @@ Int8Workspace int8_workspace(int sms) {
     const size_t slots = (size_t)sms * (kStreamWarps + 2);
     Int8Workspace w;
     w.tickets = 0;
-    // [levels][2 CTAs] (streaming), [CTAs] (chunks)
-    w.ml = align256((size_t)sms * pkv::kTreeLevels * 2 * sizeof(unsigned int));
+    // [levels][2 CTAs] (streaming), [CTAs][2 streams][4 warps] (chunks)
+    w.ml = align256((size_t)sms * std::max(pkv::kTreeLevels * 2, 2 * 4) * sizeof(unsigned int));
     w.o = w.ml + align256(slots * 4 * sizeof(float4));
     w.stream_total = w.o + slots * 256 * sizeof(float4);
     w.parts = w.ml;
