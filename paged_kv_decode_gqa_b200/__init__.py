@@ -524,7 +524,7 @@ def paged_kv_cache_read(k_out, v_out, k_cache, v_cache, slot_mapping, *, kv_dtyp
     _check(_lib.paged_kv_cache_read(
         _take("k_out", k_out, torch.float16, rows, device), _take("v_out", v_out, torch.float16, rows, device),
         kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
-        code, k_scale, v_scale, _raw_stream(stream, device)), "paged_kv_cache_read")
+        code, float(k_scale), float(v_scale), _raw_stream(stream, device)), "paged_kv_cache_read")
 
 
 def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq, *,
@@ -548,7 +548,7 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
     if len(where) not in (1, 2) or where[-1] != T:
         raise ValueError(f"positions must be [{T}] or [axes, {T}], got {tuple(where)}")
     half = inv_freq.numel()
-    sections = (half,) if sections is None else sections
+    sections = (half,) if sections is None else [int(n) for n in sections]
     if len(sections) != axes:
         raise ValueError(f"{len(sections)} sections for {axes} position axes")
     if q.dim() != 3:
@@ -570,7 +570,7 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
             _take("v_scales", v_scale, torch.float32, v_scale.shape, device), per_head, flags, st),
             "paged_kv_rope_cache_write_fp8_scaled")
         return
-    _check(lib.paged_kv_rope_cache_write(*head, sc, *sizes, code, k_scale, v_scale, flags, st),
+    _check(lib.paged_kv_rope_cache_write(*head, sc, *sizes, code, float(k_scale), float(v_scale), flags, st),
            "paged_kv_rope_cache_write")
 
 
@@ -607,7 +607,7 @@ def paged_gqa_decode_attention_int8(out, q, k_cache, v_cache, kv_scales, block_t
     if n != B:
         raise ValueError(f"{n} query rows for {B} sequences")
     _check(_lib.paged_gqa_decode_attention_int8(
-        *args, B, Hq, Hkv, D, bs, mb, NB, max_context_len, softmax_scale, ws, ws_bytes,
+        *args, B, Hq, Hkv, D, bs, mb, NB, int(max_context_len), float(softmax_scale), ws, ws_bytes,
         _raw_stream(stream, device)), "paged_gqa_decode_attention_int8")
 
 
@@ -621,6 +621,6 @@ def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_
     args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
         out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
     _check(_lib.paged_gqa_prefill_attention_int8(
-        *args, _take("query_start", query_start, torch.int32, (B + 1,), device), B, n, max_query_len, Hq, Hkv, D, bs,
-        mb, NB, max_context_len, softmax_scale, ws, ws_bytes, _raw_stream(stream, device)),
+        *args, _take("query_start", query_start, torch.int32, (B + 1,), device), B, n, int(max_query_len), Hq, Hkv, D,
+        bs, mb, NB, int(max_context_len), float(softmax_scale), ws, ws_bytes, _raw_stream(stream, device)),
         "paged_gqa_prefill_attention_int8")

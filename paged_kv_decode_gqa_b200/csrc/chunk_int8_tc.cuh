@@ -27,8 +27,8 @@
 //    scales; four warps convert them, one token (row) per thread, so that the
 //    token's scale is a register: a code becomes an exact f16 integer (a byte
 //    permute and a subtraction), and code * scale is formed in f16x2 as
-//    code * hi + (code * lo) with scale = hi + lo split into two f16, which
-//    leaves one rounding (RowScale). The f16 tiles are written in the 128-byte
+//    code * hi + (code * lo) with scale = hi + lo split into two f16, so that
+//    the scale's own rounding does not add to the value's (RowScale). The f16 tiles are written in the 128-byte
 //    swizzled layout the tensor cores read: K and V are double-buffered.
 //    Codes are finite and rows past the context get scale 0, so no row needs
 //    clearing.
@@ -87,15 +87,17 @@ struct ChunkInt8Shape {
 };
 
 // A token's scale for the conversion: scale = (hi + lo) * post, hi and lo f16. post is 1 unless the
-// scale is small (below 2^-12, where lo would lose bits to the subnormal range): then hi + lo is the
-// scale brought into [2^-7, 2^-6) and post the power of two that takes it back.
+// scale is small (below 2^-10, where lo would lose bits to the subnormal range): then hi + lo is the
+// scale brought into [2^-7, 2^-6) and post the power of two that takes it back. A value so formed is
+// off by at most 1.04 half steps of f16 (1 but for what lo loses), and by half a subnormal step more
+// where a small row's value is subnormal (a second rounding, by post).
 struct RowScale {
     __half2 hi, lo, post;
     bool small;
 };
 __device__ __forceinline__ RowScale split_scale(float s) {
     RowScale r;
-    r.small = fabsf(s) < 2.44140625e-4f && s != 0.f;
+    r.small = fabsf(s) < 9.765625e-4f && s != 0.f;
     float post = 1.f;
     if (r.small) {
         const int e = max((int)((__float_as_uint(s) >> 23) & 0xff) - 127 + 7, -24);   // post = 2^e >= 2^-24
@@ -108,7 +110,7 @@ __device__ __forceinline__ RowScale split_scale(float s) {
     r.post = __half2half2(__float2half_rn(post));
     return r;
 }
-// Four codes to four f16 of code * (hi + lo), rounded once (to within 2^-18 of a step).
+// Four codes to four f16 of code * (hi + lo).
 __device__ __forceinline__ void dequant4(uint32_t w, const RowScale& s, uint32_t& d0, uint32_t& d1) {
     uint32_t a, b;
     codes_to_half2x2(w, a, b);

@@ -34,6 +34,7 @@ namespace pkv {
 enum CacheKind { kCacheF16 = 0, kCacheFp8 = 1, kCacheInt8 = 2 };
 
 constexpr int kRopeMaxAxes = 4;
+constexpr int kMaxTokens = (1 << 30) - 1;                // of one call
 constexpr float kInt8MinAmax = 5.9604644775390625e-8f;   // 2^-24, the smallest positive binary16
 
 struct RopeWriteParams {
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const
     int64_t slot = __ldg(p.slot_mapping + tok);
     float2* turn = s_turn[threadIdx.x >> 5];
     while (tok < p.num_tokens) {
-        const int next = tok + step < p.num_tokens && tok + step >= 0 ? tok + step : p.num_tokens;
+        const int next = p.num_tokens - tok > step ? tok + step : p.num_tokens;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int j = lane + 32 * e;
@@ -348,7 +349,7 @@ struct RowWalk {
         row += drow;
         const int carry = row >= rows ? 1 : 0;
         row -= carry ? rows : 0;
-        tok = min(tok + dtok + carry, INT32_MAX / 2);    // (stays past the last token)
+        tok = min(tok + dtok + carry, kMaxTokens);       // (stays past the last token)
     }
 };
 

@@ -925,7 +925,7 @@ pkv_status check_cache_rows(const void* k_cache, const void* v_cache, const floa
         !(k_scale > 0.f && v_scale > 0.f && std::isfinite(k_scale) && std::isfinite(v_scale)))
         return PKV_ERR_INVALID_ARG;
     if (head_dim != kHeadDim || (kv_dtype == PKV_KV_INT8 && block_size != kPageRows)) return PKV_ERR_UNSUPPORTED;
-    if (num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_kv_heads > 65535 || num_tokens > pkv::kMaxTokens) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     if (!k_cache || !v_cache || !slot_mapping || !aligned16(k_cache) || !aligned16(v_cache) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))

@@ -45,6 +45,7 @@ def _chunk(**kw):
     (dict(sm=None), INVALID), (dict(k=A + 8), INVALID), (dict(vc=A + 4), INVALID), (dict(sc=A + 4), INVALID),
     (dict(sm=A + 4), INVALID), (dict(T=-1), INVALID), (dict(Hkv=0), INVALID), (dict(NB=0), INVALID),
     (dict(bs=0), INVALID), (dict(D=64), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(Hkv=70000), UNSUPPORTED),
+    (dict(T=1 << 30), UNSUPPORTED),
     (dict(T=0), OK), (dict(T=0, k=None, kc=None), OK),
 ])
 def test_write_int8_arguments(kw, status):

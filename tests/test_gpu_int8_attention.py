@@ -252,7 +252,7 @@ def test_chunk_lengths_one_by_one(n):
     c.check(c.chunk(), f"{n} new tokens")
 
 
-@pytest.mark.parametrize("kind", ["large logits", "zero scale", "negative scale", "growing", "mixed"])
+@pytest.mark.parametrize("kind", ["large logits", "zero scale", "negative scale", "growing", "mixed", "small rows"])
 @pytest.mark.parametrize("news", [[3, 5, 2], [90, 17, 300]])
 def test_chunk_value_ranges(kind, news):
     c = Case(11, 14, 2, [100, 17, 640], news, q_scale=6.0 if kind == "large logits" else 1.0)
@@ -264,6 +264,10 @@ def test_chunk_value_ranges(kind, news):
     elif kind == "mixed":
         rng = np.random.default_rng(7)
         c.scales[:, :, 1] *= np.exp2(rng.uniform(-8, 8, c.scales[:, :, 1].shape)).astype(F32)
+    elif kind == "small rows":                                        # scales around 2^-12 and down to f16's smallest
+        rng = np.random.default_rng(8)
+        c.scales *= np.exp2(rng.integers(-24, 1, c.scales.shape)).astype(F32)
+        c.scales = np.maximum(c.scales, F32(2.0 ** -24 / 127))
     c.check(c.chunk(scale=scale), kind, scale)
 
 
@@ -317,6 +321,33 @@ def test_chunk_flags_blocks_and_scales(n):
     got = c.chunk()
     assert pkv.pkv_device_error() == pkv.DEVERR_SCALE
     assert np.isfinite(got).all() and np.array_equal(got[n:], good[n:])
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_chunk_leaves_rows_behind_the_last_sequence(n):
+    """A batch padded to more rows than its sequences have: the rest of out stays as it was."""
+    c = Case(16, 28, 4, [200, 61], [n, n])
+    q, kc, vc, sc, bt, cl = c.device()
+    q = torch.cat([q, torch.full((5, 28, D), float("nan"), dtype=torch.float16, device="cuda")])
+    out = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda")
+    pkv.paged_gqa_prefill_attention_int8(out, q, kc, vc, sc, bt, cl, dev(c.qs), max_query_len=n + 3, max_context_len=208,
+                                         softmax_scale=SCALE, workspace=workspace())
+    got = host(out)
+    assert (got[2 * n:] == 7).all()
+    c.check(got[:2 * n], f"padded {n}")
+
+
+def test_chunk_many_sequences_and_ragged_items():
+    """More sequences than a block has threads, most without queries; and pieces of one KV tile."""
+    rng = np.random.default_rng(17)
+    lens = rng.integers(1, 40, 700)
+    news = np.where(rng.random(700) < 0.2, np.minimum(lens, rng.integers(1, 12, 700)), 0)
+    news[[0, 699]] = 1
+    c = Case(17, 14, 2, list(lens), list(news))
+    c.check(c.chunk(), "many sequences, narrow")
+    lens[5], news[5] = 330, 70
+    c = Case(18, 14, 2, list(lens), list(news))
+    c.check(c.chunk(), "many sequences, wide")
 
 
 # ------------------------------------------------------------------ how calls meet
