@@ -439,92 +439,59 @@ def paged_gqa_prefill_attention(out, q, k_cache, v_cache, block_tables, context_
 # The 8-bit cache (a scale per token and KV head), rotary positions with the
 # cache write, and reading a cache back.
 
-# These calls sit in a decode step's inner loop, where the host's time counts: a tensor is checked by
-# one comparison of its attributes, and the reason is worked out only when that fails.
+# These calls sit in a decode step's inner loop, where the host's time counts: the checks of their
+# tensors and the call itself are native (csrc/binding.cpp). A tensor must be dense, of its type and
+# shape, and on the current device, whose current stream is the default.
 
-def _refuse(name, t, dtype, shape, device):
-    _dense(name, t, str(dtype).replace("torch.", ""))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
+_binding = None
 
 
-def _take(name, t, dtype, shape, device):
-    """The address of `t`, a dense tensor of this type and shape on the current device."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        _refuse(name, t, dtype, shape, device)
-    return t.data_ptr()
+def _load_binding():
+    """The CPython binding, loaded on first use and bound to the CUDA library's functions."""
+    global _binding
+    import importlib.machinery
+    import importlib.util
+    import torch  # noqa: F401  (the binding's symbols come from it)
+    if not os.path.exists(BINDING_PATH):
+        raise ImportError(f"binding not built: {BINDING_PATH} is missing "
+                          "(run `python -m paged_kv_decode_gqa_b200.build`)")
+    lib = load_library()
+    loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "paged_kv_cache_write_int8", "paged_kv_cache_read", "paged_kv_rope_cache_write",
+        "paged_kv_rope_cache_write_fp8_scaled", "paged_gqa_decode_attention_int8",
+        "paged_gqa_prefill_attention_int8")))
+    _binding = module
+    return module
 
 
-_torch = _current_device = _current_stream = None
-
-
-def _runtime():
-    """torch, looked up once, and the two queries each call makes (the raw forms: the public ones build
-    a Stream object and re-check the initialisation, over a microsecond a call)."""
-    global _torch, _current_device, _current_stream
-    import torch
-    load_library()
-    _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    torch.cuda.init()
-    _torch = torch
-    return torch
-
-
-def _raw_stream(stream, device):
-    if stream is None:
-        return _current_stream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device):
-    """Checks a cache of any type: its addresses (K, V, scales), its sizes and its type code."""
+def _cache_dtype_code(kv_dtype):
     code = _CACHE_DTYPES.get(kv_dtype)
     if code is None:
         raise ValueError(f"kv_dtype must be one of {sorted(_CACHE_DTYPES)}")
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
-    dtype = torch.float16 if code == PKV_KV_F16 else torch.uint8
-    kc, vc = _take("k_cache", k_cache, dtype, shape, device), _take("v_cache", v_cache, dtype, shape, device)
-    NB, bs, Hkv, D = shape
-    sc = None
-    if code == PKV_KV_INT8:
-        if kv_scales is None:
-            raise ValueError("an int8 cache needs kv_scales")
-        sc = _take("kv_scales", kv_scales, torch.float32, (NB, Hkv, 2, bs), device)
-    elif kv_scales is not None:
-        raise ValueError("kv_scales belongs to an int8 cache")
-    return kc, vc, sc, NB, bs, Hkv, D, code
+    return code
 
 
 def paged_kv_cache_write_int8(k_new, v_new, k_cache, v_cache, kv_scales, slot_mapping, *, stream=None) -> None:
     """paged_kv_cache_write into an 8-bit cache: codes 128 + round(x / s) (uint8) and, in
     kv_scales [NB, Hkv, 2, 16] float32, s = max(max|x|, 2**-24) / 127 of every token and KV head."""
-    torch = _torch or _runtime()
-    device = _current_device()
-    kc, vc, sc, NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales, torch, device)
-    T = slot_mapping.numel()
-    rows = (T, Hkv, D)
-    _check(_lib.paged_kv_cache_write_int8(
-        _take("k_new", k_new, torch.float16, rows, device), _take("v_new", v_new, torch.float16, rows, device),
-        kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
-        _raw_stream(stream, device)), "paged_kv_cache_write_int8")
+    status = (_binding or _load_binding()).cache_write_int8(k_new, v_new, k_cache, v_cache, kv_scales, slot_mapping,
+                                                            stream)
+    if status:
+        raise PagedKVError(status, "paged_kv_cache_write_int8")
 
 
 def paged_kv_cache_read(k_out, v_out, k_cache, v_cache, slot_mapping, *, kv_dtype="f16", kv_scales=None,
                         k_scale=1.0, v_scale=1.0, stream=None) -> None:
     """k_out[i], v_out[i] ([T, Hkv, D] float16) = the cached values of slot slot_mapping[i], for an
     "f16", "fp8" or "int8" cache. Rows of negative slots are left as they were."""
-    torch = _torch or _runtime()
-    device = _current_device()
-    kc, vc, sc, NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device)
-    T = slot_mapping.numel()
-    rows = (T, Hkv, D)
-    _check(_lib.paged_kv_cache_read(
-        _take("k_out", k_out, torch.float16, rows, device), _take("v_out", v_out, torch.float16, rows, device),
-        kc, vc, sc, _take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device), T, Hkv, D, NB, bs,
-        code, float(k_scale), float(v_scale), _raw_stream(stream, device)), "paged_kv_cache_read")
+    status = (_binding or _load_binding()).cache_read(k_out, v_out, k_cache, v_cache, slot_mapping,
+                                                      _cache_dtype_code(kv_dtype), kv_scales, k_scale, v_scale, stream)
+    if status:
+        raise PagedKVError(status, "paged_kv_cache_read")
 
 
 def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq, *,
@@ -539,39 +506,12 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
     (j, j + rotary_dim / 2). For an "fp8" cache k_scale and v_scale are numbers, or float32 CUDA
     tensors of 1 or Hkv elements.
     """
-    torch = _torch or _runtime()
-    device = _current_device()
-    kc, vc, sc, NB, bs, Hkv, D, code = _cache(k_cache, v_cache, kv_dtype, kv_scales, torch, device)
-    T = slot_mapping.numel()
-    where = positions.shape
-    axes = where[0] if len(where) == 2 else 1
-    if len(where) not in (1, 2) or where[-1] != T:
-        raise ValueError(f"positions must be [{T}] or [axes, {T}], got {tuple(where)}")
-    half = inv_freq.numel()
-    sections = (half,) if sections is None else [int(n) for n in sections]
-    if len(sections) != axes:
-        raise ValueError(f"{len(sections)} sections for {axes} position axes")
-    if q.dim() != 3:
-        raise ValueError("q must be [T, num_q_heads, head_dim]")
-    Hq = q.shape[1]
-    rows, kv_rows = (T, Hq, D), (T, Hkv, D)
     flags = (PKV_ROPE_INTERLEAVED if interleaved else 0) | (PKV_ROPE_CYCLIC_AXES if cyclic_axes else 0)
-    f16, lib, st = torch.float16, _lib, _raw_stream(stream, device)
-    head = (_take("q_out", q_out, f16, rows, device), _take("q", q, f16, rows, device),
-            _take("k_new", k_new, f16, kv_rows, device), _take("v_new", v_new, f16, kv_rows, device), kc, vc)
-    sizes = (_take("slot_mapping", slot_mapping, torch.int64, slot_mapping.shape, device),
-             _take("positions", positions, torch.int64, where, device),
-             _take("inv_freq", inv_freq, torch.float32, inv_freq.shape, device),
-             T, Hq, Hkv, D, 2 * half, axes, (_i32 * max(axes, 1))(*sections), NB, bs)
-    if code == PKV_KV_FP8_E4M3 and hasattr(k_scale, "data_ptr"):
-        per_head = _scales(k_scale, v_scale, Hkv)
-        _check(lib.paged_kv_rope_cache_write_fp8_scaled(
-            *head, *sizes, _take("k_scales", k_scale, torch.float32, k_scale.shape, device),
-            _take("v_scales", v_scale, torch.float32, v_scale.shape, device), per_head, flags, st),
-            "paged_kv_rope_cache_write_fp8_scaled")
-        return
-    _check(lib.paged_kv_rope_cache_write(*head, sc, *sizes, code, float(k_scale), float(v_scale), flags, st),
-           "paged_kv_rope_cache_write")
+    status = (_binding or _load_binding()).rope_cache_write(
+        q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq, sections, flags,
+        _cache_dtype_code(kv_dtype), kv_scales, k_scale, v_scale, stream)
+    if status:
+        raise PagedKVError(status, "paged_kv_rope_cache_write")
 
 
 def paged_gqa_decode_workspace_size_int8() -> int:
@@ -579,36 +519,15 @@ def paged_gqa_decode_workspace_size_int8() -> int:
     return int(load_library().paged_gqa_decode_workspace_size_int8())
 
 
-def _int8_attention(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device):
-    """Checks what decode and chunk attention share: the addresses in call order, and the sizes."""
-    kc, vc, sc, NB, bs, Hkv, D, _ = _cache(k_cache, v_cache, "int8", kv_scales, torch, device)
-    if q.dim() != 3 or block_tables.dim() != 2:
-        raise ValueError("q must be [rows, num_q_heads, head_dim] and block_tables [batch, max_blocks]")
-    n, Hq, _ = q.shape
-    B, mb = block_tables.shape
-    rows = (n, Hq, D)
-    if workspace.dtype is not torch.uint8:
-        _dense("workspace", workspace, "uint8", "float32", "int32")
-    ws = _take("workspace", workspace, workspace.dtype, workspace.shape, device)
-    return ((_take("out", out, torch.float16, rows, device), _take("q", q, torch.float16, rows, device), kc, vc, sc,
-             _take("block_tables", block_tables, torch.int32, (B, mb), device),
-             _take("context_lens", context_lens, torch.int32, (B,), device)),
-            n, Hq, Hkv, D, NB, bs, B, mb, ws, workspace.numel() * workspace.element_size())
-
-
 def paged_gqa_decode_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, *,
                                     max_context_len, softmax_scale, workspace, stream=None) -> None:
     """paged_gqa_decode_attention over an 8-bit cache (load-balanced plan; a zero-filled workspace of
     paged_gqa_decode_workspace_size_int8() bytes, reusable)."""
-    torch = _torch or _runtime()
-    device = _current_device()
-    args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
-        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
-    if n != B:
-        raise ValueError(f"{n} query rows for {B} sequences")
-    _check(_lib.paged_gqa_decode_attention_int8(
-        *args, B, Hq, Hkv, D, bs, mb, NB, int(max_context_len), float(softmax_scale), ws, ws_bytes,
-        _raw_stream(stream, device)), "paged_gqa_decode_attention_int8")
+    status = (_binding or _load_binding()).decode_attention_int8(
+        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, max_context_len, softmax_scale, workspace,
+        stream)
+    if status:
+        raise PagedKVError(status, "paged_gqa_decode_attention_int8")
 
 
 def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, *,
@@ -616,11 +535,8 @@ def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_
     """paged_gqa_prefill_attention over an 8-bit cache: query rows q [total, Hq, D] of each sequence
     (query_start [B+1] int32), the last n_b tokens of its context, attending causally; a zero-filled
     workspace of paged_gqa_prefill_workspace_size(Hq, Hkv, D, "int8") bytes, reusable."""
-    torch = _torch or _runtime()
-    device = _current_device()
-    args, n, Hq, Hkv, D, NB, bs, B, mb, ws, ws_bytes = _int8_attention(
-        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, workspace, torch, device)
-    _check(_lib.paged_gqa_prefill_attention_int8(
-        *args, _take("query_start", query_start, torch.int32, (B + 1,), device), B, n, int(max_query_len), Hq, Hkv, D,
-        bs, mb, NB, int(max_context_len), float(softmax_scale), ws, ws_bytes, _raw_stream(stream, device)),
-        "paged_gqa_prefill_attention_int8")
+    status = (_binding or _load_binding()).prefill_attention_int8(
+        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, max_query_len, max_context_len,
+        softmax_scale, workspace, stream)
+    if status:
+        raise PagedKVError(status, "paged_gqa_prefill_attention_int8")

@@ -1,10 +1,12 @@
-"""Builds the CUDA library in-tree: paged_kv_decode_gqa_b200/libpagedkv_b200.so.
+"""Builds the CUDA library and the CPython binding in-tree: paged_kv_decode_gqa_b200/libpagedkv_b200.so
+and paged_kv_decode_gqa_b200/_binding.so.
 
     python -m paged_kv_decode_gqa_b200.build [--force] [--verbose-ptxas]
 
 nvcc compiles the single translation unit csrc/pagedkv.cu for sm_100a only,
 links the CUDA runtime statically and nothing else (the TMA descriptor entry
-point is fetched from the driver at run time).
+point is fetched from the driver at run time). g++ compiles csrc/binding.cpp against the
+headers of the PyTorch in use.
 """
 from __future__ import annotations
 
@@ -12,12 +14,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpagedkv_b200.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -34,14 +38,37 @@ def sources():
                   + [os.path.join(INCLUDE, "pagedkv.h")])
 
 
+def _older(target, files) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(s) > os.path.getmtime(target) for s in files)
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
+    return _older(LIB, sources())
+
+
+def build_binding(force: bool = False) -> str:
+    """The binding, when it is older than its sources. It belongs to one Python and one PyTorch."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _older(BINDING, [src, os.path.join(INCLUDE, "pagedkv.h")]):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += ["-o", tmp, src, "-L", libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_binding(force)
     if not force and not is_stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

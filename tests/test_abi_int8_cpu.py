@@ -121,3 +121,15 @@ def test_the_8_bit_type_is_refused_where_it_is_not_named():
                                           None) == INVALID
     with pytest.raises(ValueError):
         pkv.kv_dtype_code("int8")
+
+
+def test_the_binding_refuses_what_is_not_a_dense_cuda_tensor():
+    import torch
+    x, caches = torch.zeros(1, 2, 128, dtype=torch.float16), torch.zeros(2, 16, 2, 128, dtype=torch.uint8)
+    scales, slots = torch.zeros(2, 2, 2, 16), torch.zeros(1, dtype=torch.int64)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        pkv.paged_kv_cache_write_int8(x, x, caches, caches, scales, slots)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        pkv.paged_kv_cache_write_int8(x, x, None, caches, scales, slots)
+    with pytest.raises(ValueError, match="kv_dtype"):
+        pkv.paged_kv_cache_read(x, x, caches, caches, slots, kv_dtype="int4")
