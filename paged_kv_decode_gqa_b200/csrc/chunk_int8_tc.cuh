@@ -21,22 +21,39 @@
 //    warps w and w + 4 share its lanes).
 //  * Load balance: the items (query group, KV head, sequence) form a row of
 //    KV tiles, every CTA takes an equal run of it, an item cut between CTAs is
-//    computed in pieces that store (max, sum, O) per row, and the piece that
-//    takes the last ticket merges them. Nobody waits on another CTA.
-//  * Staging: two TMA warps bring pages of codes (128-byte swizzle) and their
-//    scales; four warps convert them, one token (row) per thread, so that the
-//    token's scale is a register: a code becomes an exact f16 integer (a byte
-//    permute and a subtraction), and code * scale is formed in f16x2 as
-//    code * hi + (code * lo) with scale = hi + lo split into two f16, so that
-//    the scale's own rounding does not add to the value's (RowScale). The f16 tiles are written in the 128-byte
-//    swizzled layout the tensor cores read: K and V are double-buffered.
-//    Codes are finite and rows past the context get scale 0, so no row needs
-//    clearing.
+//    computed in pieces that store (max, sum, O) per row, and whoever takes the
+//    last ticket merges them in their order: wide warp by warp behind the next
+//    item's products, narrow all warps of the CTA at its end. Nobody waits on
+//    another CTA.
+//  * Staging: one TMA warp brings the codes of K (128-byte swizzle), the scales
+//    and Q, one the codes of V; four warps convert them, one token (row) per
+//    thread, so that the token's scale is a register: a code becomes an exact
+//    f16 integer (a byte permute and a subtraction), and code * scale is formed
+//    in f16x2 as code * hi + (code * lo) with scale = hi + lo split into two
+//    f16, so that the scale's own rounding does not add to the value's
+//    (RowScale). The f16 tiles are written in the 128-byte swizzled layout the
+//    tensor cores read: K and V are double-buffered. Codes are finite and rows
+//    past the context get scale 0, so no row needs clearing.
 //  * Softmax: a row per thread. The running maximum (exp2 domain) is raised
 //    only by more than 8, so most tiles rescale nothing; the row sum adds the
-//    probabilities as rounded to f16. Warps with no live row do no work.
+//    fp32 probabilities before they are rounded to f16 for P V. Warps with no
+//    live row do no work.
 // Every wait is bounded; one that runs out flags PKV_DEVERR_WAIT_TIMEOUT and
 // every role stops, drains what it has in flight and leaves; TMEM is freed.
+//
+// Measured at 28 / 4 heads: 512 new tokens of 8 sequences on 2048-token contexts
+// 160 us, 0.40 of the measured dense rate; 5 new tokens of 64 sequences on
+// contexts of 32 to 2048 tokens 54 us. Bound: neither memory nor the tensor cores but
+// the chain S -> softmax -> P V of a stream, about 4500 cycles per KV tile of
+// which the products are 2300, on an SM whose shared memory is busy for 2560 of
+// them (operands 1536, conversion 768, TMA 256). Tried and not kept, us for the
+// two: logits in halves of 64 tokens, double-buffered, one issuing warp 212 / 58
+// (the products of N = 64 read Q twice); the same with an issuing warp per
+// stream 154 / 59; logits taken out of TMEM at once and P in its own columns
+// 164 / 62; an issuing warp per stream with N = 128 172 / 54 (the streams run
+// in step and wait for the same units); one pass over each half's logits 160 /
+// 54; 16 TMEM columns per load instead of 64, 182 (against 167 then); eight
+// converter warps at 96 registers a thread 167 / 61.
 #pragma once
 
 #include "int8_cache.cuh"
@@ -78,7 +95,7 @@ struct ChunkInt8Shape {
     static constexpr int kSmemBytes = kOffWords + 256;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one SM");
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kConvertWarp = 8;              // 8..11 (eight converters leave the softmax 96 registers: slower)
+    static constexpr int kConvertWarp = 8;              // 8..11
     static constexpr int kTmaKWarp = 12, kTmaVWarp = 13, kMmaWarp = 14;
     static constexpr int kThreads = 32 * 15;
     static constexpr uint32_t kTmemCols = 512;
@@ -912,7 +929,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // 0's release-acquire; the loads of the last one, which merges, follow its acquire:
             // out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of the pieces, whoever merges.
             // The other warps go on meanwhile. (Merged at the CTA's end as below, 512 tokens on 8 x 2048
-            // contexts took 171 us instead of 162; narrow chunks have few rows, hence few warps, for this.)
+            // contexts took 171 us instead of 160; narrow chunks have few rows, hence few warps, for this.)
             __syncwarp();
             const int c_first = cta_of(pc.u), c_last = cta_of(pc.u + pc.ntiles - 1);
             unsigned int* tick = p.tickets + ((int64_t)c_last * 2 + t) * 4 + quarter;

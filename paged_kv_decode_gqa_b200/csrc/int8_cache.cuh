@@ -24,7 +24,10 @@
 // off by 2^-4 radians.
 // Rounding: fp32 throughout, once to f16, to E4M3 (of x / scale, an IEEE
 // division, as paged_kv_cache_write) or to the 8-bit code.
-// Bound: HBM; every row is read and written once.
+// Bound: HBM; every row is read and written once. Measured at 28 / 4 heads: f16,
+// 16384 tokens 52.9 us, 5.7 TB/s (0.87 of the measured copy rate); E4M3, 2049
+// tokens 5.9 us and f16, 128 tokens 2.8 us, where the launch and one round
+// trip to memory take most of it.
 #pragma once
 
 #include "cache_write.cuh"
@@ -354,7 +357,8 @@ struct RowWalk {
 };
 
 // The write without rotation into an 8-bit cache: the K and V rows of all tokens in one run; a thread
-// keeps kRowBatch rows in flight and refills each as soon as it is done.
+// keeps kRowBatch rows in flight and refills each as soon as it is done. Bound: HBM; 16411 tokens of 4 KV heads
+// written and read back (two launches, 102 MB) take 26.6 us, 0.59 of the measured copy rate.
 __global__ void __launch_bounds__(256, 4) cache_write_int8_kernel(const RopeWriteParams p) {
     const int i = threadIdx.x & 7;
     const int64_t groups = (int64_t)gridDim.x * 32;
