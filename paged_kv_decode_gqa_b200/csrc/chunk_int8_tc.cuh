@@ -3,9 +3,13 @@
 //
 // What it computes: query i of sequence b sits at position L_b - n_b + i and
 // attends causally to positions [0, p] of the sequence's 8-bit cache
-// (int8_cache.cuh), query head h reading KV head h / G. A cached value is
-// (code - 128) * scale, rounded to f16 as it is staged for the tensor cores
-// (half a step, 2^-11; values past the f16 range saturate).
+// (int8_cache.cuh), query head h reading KV head h / G. A key enters the
+// products as its codes less 128, exact in f16, and its scale as a factor of
+// the logit in fp32. A cached value is (code - 128) * scale, rounded to f16 as
+// it is staged for the tensor cores (half a step, 2^-11; values past the f16
+// range saturate). (With the keys rounded to f16 as well the output's error
+// was 0.00032 of its norm, where f16 outputs alone are off by 0.00019; it is
+// 0.00025 so, at the same speed.)
 //
 // Structure (one CTA per SM, persistent):
 //  * A query tile is T = floor(128 / G) query tokens x the G heads of one KV
@@ -27,33 +31,38 @@
 //    another CTA.
 //  * Staging: one TMA warp brings the codes of K (128-byte swizzle), the scales
 //    and Q, one the codes of V; four warps convert them, one token (row) per
-//    thread, so that the token's scale is a register: a code becomes an exact
-//    f16 integer (a byte permute and a subtraction), and code * scale is formed
-//    in f16x2 as code * hi + (code * lo) with scale = hi + lo split into two
-//    f16, so that the scale's own rounding does not add to the value's
+//    thread: a code becomes an exact f16 integer (a byte permute and a
+//    subtraction), and for V, whose scale is thus a register, code * scale is
+//    formed in f16x2 as code * hi + (code * lo) with scale = hi + lo split into
+//    two f16, so that the scale's own rounding does not add to the value's
 //    (RowScale). The f16 tiles are written in the 128-byte swizzled layout the
 //    tensor cores read: K and V are double-buffered. Codes are finite and rows
 //    past the context get scale 0, so no row needs clearing.
-//  * Softmax: a row per thread. The running maximum (exp2 domain) is raised
-//    only by more than 8, so most tiles rescale nothing; the row sum adds the
-//    fp32 probabilities before they are rounded to f16 for P V. Warps with no
-//    live row do no work.
+//  * Softmax: a row per thread, half a KV tile at a time, on logits read from
+//    TMEM once. The running maximum (exp2 domain) is raised only by more than
+//    8 (15 in a tile's second half), so most tiles rescale nothing; the row sum
+//    adds the fp32 probabilities before they are rounded to f16 for P V. Warps
+//    with no live row do no work.
 // Every wait is bounded; one that runs out flags PKV_DEVERR_WAIT_TIMEOUT and
 // every role stops, drains what it has in flight and leaves; TMEM is freed.
 //
 // Measured at 28 / 4 heads: 512 new tokens of 8 sequences on 2048-token contexts
-// 160 us, 0.40 of the measured dense rate; 5 new tokens of 64 sequences on
-// contexts of 32 to 2048 tokens 54 us. Bound: neither memory nor the tensor cores but
-// the chain S -> softmax -> P V of a stream, about 4500 cycles per KV tile of
+// 164 us, 0.39 of the measured dense rate; 5 new tokens of 64 sequences on
+// contexts of 32 to 2048 tokens 56 us. Bound: neither memory nor the tensor cores
+// but the chain S -> softmax -> P V of a stream, about 4500 cycles per KV tile of
 // which the products are 2300, on an SM whose shared memory is busy for 2560 of
-// them (operands 1536, conversion 768, TMA 256). Tried and not kept, us for the
-// two: logits in halves of 64 tokens, double-buffered, one issuing warp 212 / 58
-// (the products of N = 64 read Q twice); the same with an issuing warp per
-// stream 154 / 59; logits taken out of TMEM at once and P in its own columns
-// 164 / 62; an issuing warp per stream with N = 128 172 / 54 (the streams run
-// in step and wait for the same units); one pass over each half's logits 160 /
-// 54; 16 TMEM columns per load instead of 64, 182 (against 167 then); eight
-// converter warps at 96 registers a thread 167 / 61.
+// them (operands 1536, conversion 768, TMA 256); and the instruction cache, which
+// the roles compete for. Tried and not kept, us for the two, against 160 / 54 of
+// the form they started from (keys rounded to f16): logits in halves of 64 tokens,
+// double-buffered, one issuing warp 212 / 58 (products of N = 64 read Q twice); the
+// same with an issuing warp per stream 154 / 59; logits taken out of TMEM at once
+// and P in its own columns 164 / 62; an issuing warp per stream with N = 128
+// 172 / 54 (the streams run in step and wait for the same units); 16 TMEM columns
+// per load instead of 64, 182 (against 167 then); eight converter warps 167 / 61.
+// Against 164 / 56 of the present form: the waits' slow path inlined 176 / 65;
+// registers moved to the softmax (setmaxnreg, inlined waits) 170 / 63; the scales
+// brought in by a warp of their own 195 / 71; four warps each for K and V 183 / 67;
+// the conversion rolled up to 16 channels 174 / 63.
 #pragma once
 
 #include "int8_cache.cuh"
@@ -73,8 +82,7 @@ struct ChunkInt8Params {
     int32_t Hq, Hkv, G;
     int32_t max_blocks_per_seq, num_blocks, max_context_len;
     int32_t tokens;               // T: query tokens of a tile
-    float logit_scale_log2;       // |softmax_scale| * log2(e), or 1 when that is 0 (masked logits are -inf)
-    float key_sign;               // sign of softmax_scale (0 for 0), applied to the keys
+    float logit_scale_log2;       // softmax_scale * log2(e)
 };
 
 struct ChunkInt8Shape {
@@ -83,23 +91,27 @@ struct ChunkInt8Shape {
     static constexpr int kTile = 2 * kChunk;            // a 128 x 128 f16 tile
     static constexpr int kRaw = 128 * 128;              // codes of K or V of a KV tile
     static constexpr int kScales = 8 * 128;             // scales of a KV tile: 8 pages x (16 K, 16 V)
-    static constexpr int kBarBytes = 256;
-    // Q A | Q B or a second raw stage | K x 2 | V x 2 | raw K, V | scales x 2 | barriers and words.
+    static constexpr int kBarBytes = 320;
+    static constexpr int kFactors = 128 * 4;            // logit factors of a KV tile's tokens
+    static constexpr int kFactorSlots = 3;
+    // Q A | Q B or a second raw stage | K x 2 | V x 2 | raw K, V | scales | factors x 3 | barriers and words.
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + 2 * kTile;
     static constexpr int kOffRaw = kOffV + 2 * kTile;
     static constexpr int kOffScales = kOffRaw + 2 * kRaw;
-    static constexpr int kOffBars = kOffScales + 2 * kScales;
-    static constexpr int kOffWords = kOffBars + kBarBytes;   // block scan [20], first sequence [2], abort flag, a barrier
-    static constexpr int kSmemBytes = kOffWords + 256;
+    static constexpr int kOffFactors = kOffScales + kScales;
+    static constexpr int kOffBars = kOffFactors + kFactorSlots * kFactors;
+    static constexpr int kOffWords = kOffBars + kBarBytes;   // first sequence [2], abort flag, cut items
+    static constexpr int kSmemBytes = kOffWords + 96;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one SM");
     static constexpr int kSoftmaxWarps = 8;
     static constexpr int kConvertWarp = 8;              // 8..11
     static constexpr int kTmaKWarp = 12, kTmaVWarp = 13, kMmaWarp = 14;
     static constexpr int kThreads = 32 * 15;
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr float kRescaleThreshold = 8.f;
+    // log2 of the largest probability of a KV tile's first half (64 tokens), and of its second half: f16 holds it
+    static constexpr float kRescaleThreshold = 8.f, kSecondThreshold = 15.f;
     static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
 };
 
@@ -127,14 +139,10 @@ __device__ __forceinline__ RowScale split_scale(float s) {
     r.post = __half2half2(__float2half_rn(post));
     return r;
 }
-// Four codes to four f16 of code * (hi + lo).
-__device__ __forceinline__ void dequant4(uint32_t w, const RowScale& s, uint32_t& d0, uint32_t& d1) {
-    uint32_t a, b;
-    codes_to_half2x2(w, a, b);
-    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&b);
-    const __half2 u = __hfma2(x, s.hi, __hmul2(x, s.lo)), v = __hfma2(y, s.hi, __hmul2(y, s.lo));
-    d0 = *reinterpret_cast<const uint32_t*>(&u);
-    d1 = *reinterpret_cast<const uint32_t*>(&v);
+// Two integers times (hi + lo), rounded to f16.
+__device__ __forceinline__ uint32_t scaled(uint32_t a, const RowScale& s) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), u = __hfma2(x, s.hi, __hmul2(x, s.lo));
+    return *reinterpret_cast<const uint32_t*>(&u);
 }
 __device__ __forceinline__ uint32_t times(uint32_t a, __half2 f) {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
@@ -170,6 +178,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+// 32 factors (pairs) at shared address `f`.
+__device__ __forceinline__ void load_factors(uint32_t f, uint64_t (&v)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2)
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[e]), "=l"(v[e + 1]) : "r"(f + 8 * e) : "memory");
+}
+// x[e] = x[e] * factor[e] + m over 32 tokens from q on.
+template <int kCols>
+__device__ __forceinline__ void relative_logits(float (&x)[kCols], int q, const uint64_t (&v)[16], uint64_t m) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        unpack_f32x2(fma_f32x2(pack_f32x2(x[q + 2 * e], x[q + 2 * e + 1]), v[e], m), x[q + 2 * e], x[q + 2 * e + 1]);
 }
 // Logits of consecutive tokens, those past number `left` hidden.
 template <int kCols>
@@ -237,6 +258,25 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[64]) {
     tmem_ld32x2(taddr, *reinterpret_cast<float (*)[32]>(&v[0]), taddr + 32, *reinterpret_cast<float (*)[32]>(&v[32]));
 }
 
+// The rest of a bounded wait, out of line (the many places that wait would fill the instruction cache with it):
+// false, and the abort flag at shared address `abort` set, when the limit has run out, or another role's has.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t abort) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 63u) {
+            uint32_t given_up;
+            asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(given_up) : "r"(abort) : "memory");
+            if (given_up) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                flag_error(PKV_DEVERR_WAIT_TIMEOUT);
+                asm volatile("st.volatile.shared.u32 [%0], %1;" :: "r"(abort), "r"(1u) : "memory");
+                return false;
+            }
+        }
+    }
+}
+
 template <bool kNarrow>
 __global__ void __launch_bounds__(ChunkInt8Shape::kThreads, 1)
 chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -255,13 +295,13 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         flag_error(PKV_DEVERR_WAIT_TIMEOUT);             // never seen: no operand tile could be addressed
         return;
     }
-    long long* s_red = reinterpret_cast<long long*>(smem_raw + S::kOffWords);     // [20]
-    long long* s_first = s_red + 20;                                              // [2]
+    long long* s_red = reinterpret_cast<long long*>(smem_raw + S::kOffFactors);   // [15], before the first factors
+    long long* s_first = reinterpret_cast<long long*>(smem_raw + S::kOffWords);   // [2]
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_first + 2);
     // the items this CTA holds a piece of, as the softmax meets them
     struct CutItem { long long u; int row0, nq, g, ntiles; };
-    CutItem* s_cut = reinterpret_cast<CutItem*>(smem_raw + S::kOffWords + 200);   // [2]
-    int* s_cuts = reinterpret_cast<int*>(smem_raw + S::kOffWords + 248);          // how many
+    CutItem* s_cut = reinterpret_cast<CutItem*>(smem_raw + S::kOffWords + 32);    // [2]
+    int* s_cuts = reinterpret_cast<int*>(smem_raw + S::kOffWords + 20);           // how many
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.G, T = p.tokens;
     const int per_item = kQTiles * T;                    // query tokens of an item
@@ -419,7 +459,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // raw stage 0 has its own place, stage 1 (narrow) that of the second query tile
     auto raw_k = [&](int s) { return base + (s ? S::kOffQ + S::kTile : S::kOffRaw); };
     auto raw_v = [&](int s) { return raw_k(s) + S::kRaw; };
-    auto raw_sc = [&](int s) { return base + S::kOffScales + s * S::kScales; };
+    const uint32_t raw_sc = base + S::kOffScales;
+    auto factors = [&](int s) { return base + S::kOffFactors + s * S::kFactors; };
     const uint32_t bars = base + S::kOffBars;
     const uint32_t q_full = bars, q_empty = bars + 8, drain = bars + 16;
     auto s_full = [&](int t) { return bars + 24 + 8u * t; };
@@ -437,7 +478,11 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // narrow: the odd stream's (m, l) of a piece are in TMEM; the even stream has read them
     const uint32_t x_full = bars + 216, x_read = bars + 224;
     const uint32_t tmem_slot = bars + 248;
-    const uint32_t merge_bar = base + S::kOffWords + 192;
+    // scales of a KV tile: raw, and as the logit factors of its tokens; O_t has the first half of P V
+    const uint32_t rs_full = bars + 256, rs_empty = bars + 264;
+    auto f_full = [&](int s) { return bars + 272 + 8u * s; };
+    auto o_half = [&](int t) { return bars + 296 + 8u * t; };
+    const uint32_t merge_bar = bars + 312;
     const int rows = G * T;                              // rows of Q the TMA fills; the rest stay zero
     if (threadIdx.x == 0) {
         *s_abort = 0;
@@ -445,6 +490,9 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         mbar_init(x_full, 128);
         mbar_init(x_read, 128);
         mbar_init(merge_bar, 1);
+        mbar_init(rs_full, 1);
+        mbar_init(rs_empty, 4);
+        for (int s = 0; s < S::kFactorSlots; ++s) mbar_init(f_full(s), 4);
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(drain, 1);
@@ -453,6 +501,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             mbar_init(p_full(t, 0), 128);
             mbar_init(p_full(t, 1), 128);
             mbar_init(o_done(t), 1);
+            mbar_init(o_half(t), 1);
             mbar_init(o_free(t), 128);
             mbar_init(k_full(t), 4);
             mbar_init(k_empty(t), 1);
@@ -486,19 +535,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
     // Bounded wait that also gives up once another role has given up.
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = global_timer_ns();
-        for (uint32_t it = 0;; ++it) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if ((it & 63u) == 63u) {
-                if (*s_abort) return false;
-                if (global_timer_ns() - t0 > kWaitLimitNs) {
-                    flag_error(PKV_DEVERR_WAIT_TIMEOUT);
-                    *s_abort = 1;
-                    return false;
-                }
-            }
-        }
+        return mbar_try_wait(bar, parity) || wait_longer(bar, parity, base + S::kOffWords + 16);
     };
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
@@ -515,7 +552,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         auto full = [&](int s) { return is_k ? rk_full(s) : rv_full(s); };
         auto empty = [&](int s) { return is_k ? rk_empty(s) : rv_empty(s); };
-        int gj = 0, k = 0;
+        int gj = 0, k = 0, scales_short = 0;             // KV tiles, pieces; a tile whose scales were not asked for
         bool ok = true;
         Cursor cu = start;
         Piece pc;
@@ -535,15 +572,28 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                 }
                 if (gj >= kRawStages && !(ok = wait_all(empty(s), ((gj / kRawStages) - 1) & 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(full(s), pages * (2048 + (is_k ? 128 : 0)));
+                if (lane == 0) mbar_arrive_expect_tx(full(s), pages * 2048);
                 __syncwarp();
                 if (lane < pages) {
                     fence_proxy_async_shared();          // the converters' reads of the stage come first
                     const uint32_t dst = (is_k ? raw_k(s) : raw_v(s)) + lane * 2048;
                     tma_load_3d_reused(dst, map, full(s), 0, pc.g, pb * kPageRows);
-                    if (is_k) tma_load_3d_reused(raw_sc(s) + lane * 128, &tm_s, full(s), 0, pc.g, pb);
                 }
                 __syncwarp();
+                if (is_k) {                              // the scales' one stage, behind the codes
+                    if (gj >= 1 && !(ok = wait_all(rs_empty, (gj - 1) & 1))) {
+                        ++gj;
+                        ++scales_short;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(rs_full, pages * 128);
+                    __syncwarp();
+                    if (lane < pages) {
+                        fence_proxy_async_shared();
+                        tma_load_3d_reused(raw_sc + lane * 128, &tm_s, rs_full, 0, pc.g, pb);
+                    }
+                    __syncwarp();
+                }
                 if (is_k && j == pc.j0) {                // the piece's Q, behind its first K
                     if (k >= 1 && !(ok = wait_all(q_empty, (k - 1) & 1))) {
                         ++gj;
@@ -563,14 +613,15 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         // nothing of ours may be in flight when the CTA leaves
         for (int j = max(0, gj - kRawStages); j < gj; ++j) mbar_wait(full(j % kRawStages), (j / kRawStages) & 1);
+        if (is_k && gj > scales_short) mbar_wait(rs_full, (gj - scales_short - 1) & 1);
         if (is_k && k >= 1) mbar_wait(q_full, (k - 1) & 1);
     } else if (warp >= S::kConvertWarp && warp < S::kConvertWarp + 4) {
         // ========================= codes to f16 tiles: a token per thread =========================
         const int row = 32 * (warp & 3) + lane;                    // token of the KV tile
         const uint32_t sw = (uint32_t)(row & 7);
-        // converts the raw tile at `src` with this row's scale into the f16 tile at `dst`, 64 channels at
-        // a time (kept as a loop: the roles' code competes for the instruction cache)
-        auto convert = [&](uint32_t src, uint32_t dst, float scale) {
+        // the raw tile at `src` into the f16 tile at `dst`, 64 channels at a time (kept as a loop: the roles' code
+        // competes for the instruction cache): K as the codes' integers, V times this row's scale
+        auto convert = [&](bool is_k, uint32_t src, uint32_t dst, float scale) {
             const RowScale s = split_scale(scale);
             const bool any_small = __any_sync(0xffffffffu, s.small);
             const uint32_t in = src + row * 128, out = dst + row * 128;
@@ -582,13 +633,17 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {                      // 16 channels
                     uint32_t d[8];
-                    dequant4(w[c].x, s, d[0], d[1]);
-                    dequant4(w[c].y, s, d[2], d[3]);
-                    dequant4(w[c].z, s, d[4], d[5]);
-                    dequant4(w[c].w, s, d[6], d[7]);
-                    if (any_small) {
+                    codes_to_half2x2(w[c].x, d[0], d[1]);
+                    codes_to_half2x2(w[c].y, d[2], d[3]);
+                    codes_to_half2x2(w[c].z, d[4], d[5]);
+                    codes_to_half2x2(w[c].w, d[6], d[7]);
+                    if (!is_k) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] = times(d[e], s.post);
+                        for (int e = 0; e < 8; ++e) d[e] = scaled(d[e], s);
+                        if (any_small) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) d[e] = times(d[e], s.post);
+                        }
                     }
                     const uint32_t o = out + h * S::kChunk;
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
@@ -598,21 +653,32 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
             }
         };
-        // the row's scale: 0 past the context; outside [0, 2^60] flagged and 0; saturating at the f16 range
+        // the row's scale: 0 past the context; outside [0, 2^60] flagged and 0
         auto row_scale = [&](const Piece& pc, int j, uint32_t addr) -> float {
             const float s = lds32(addr);
             const bool live = j * S::kKvTok + row < min(pc.L, pc.npages * kPageRows);
             const bool fine = s >= 0.f && s <= kScaleMax;
             if (live && !fine) flag_error(PKV_DEVERR_SCALE);
-            return live && fine ? fminf(s, 511.75f) : 0.f;
+            return live && fine ? s : 0.f;
         };
         const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4);
-        // stages the K (or V) of KV tile g, its j-th of the item, with this row's scale; false when a wait ran out
-        auto stage_tile = [&](bool is_k, int g, float scale) -> bool {
+        // stages the K (with its tokens' logit factors) or V of KV tile g, the piece's `first` or not; false when a
+        // wait ran out
+        auto stage_tile = [&](bool is_k, int g, bool first, float scale) -> bool {
             const int s = g % kRawStages, d = g & 1;
-            if (!is_k && !wait_all(rv_full(s), (g / kRawStages) & 1)) return false;
+            if (!wait_all(is_k ? rk_full(s) : rv_full(s), (g / kRawStages) & 1)) return false;
             if (g >= 2 && !wait_all(is_k ? k_empty(d) : v_empty(d), ((g >> 1) - 1) & 1)) return false;
-            convert(is_k ? raw_k(s) : raw_v(s), is_k ? k_s(d) : v_s(d), scale);
+            if (is_k) {
+                // Tile g - 3, whose slot this is, has left the softmax: wide, as both streams' S of tile g - 2 is
+                // there; narrow, when its P V is done. (A piece's first K comes behind V of tile g - 1, which waited
+                // for just that, and whose own P V may have taken the barrier a phase further by now.)
+                if (kNarrow && !first && g >= 3 && !wait_all(v_empty(d ^ 1), ((g - 3) >> 1) & 1)) return false;
+                const int slot = g % S::kFactorSlots;
+                asm volatile("st.shared.f32 [%0], %1;" :: "r"(factors(slot) + 4 * row), "f"(scale) : "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(f_full(slot));
+            }
+            convert(is_k, is_k ? raw_k(s) : raw_v(s), is_k ? k_s(d) : v_s(d), scale);
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
@@ -632,15 +698,16 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int step = 0; step < 2 * n; ++step) {
                 const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
                 const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
-                const int s = (gj + i) % kRawStages;
                 float scale = v_scale;
                 if (is_k) {
-                    if (!(ok = wait_all(rk_full(s), ((gj + i) / kRawStages) & 1))) break;
-                    scale = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off) * p.key_sign;
-                    v_next = row_scale(pc, pc.j0 + i, raw_sc(s) + sc_off + 64);
+                    if (!(ok = wait_all(rs_full, (gj + i) & 1))) break;
+                    scale = row_scale(pc, pc.j0 + i, raw_sc + sc_off) * p.logit_scale_log2;
+                    v_next = fminf(row_scale(pc, pc.j0 + i, raw_sc + sc_off + 64), 511.75f);   // at the f16 range
                     if (i == 0) v_scale = v_next;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rs_empty);
                 }
-                if (!(ok = stage_tile(is_k, gj + i, scale))) break;
+                if (!(ok = stage_tile(is_k, gj + i, i == 0, scale))) break;
                 if (!is_k) v_scale = v_next;
             }
             gj += n;
@@ -670,8 +737,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tc_fence_after();
                 umma_half_ts(tmem_o(t), tmem_s(t) + 32 * h, umma_desc_sw128(v_s(s) + 8192 * h, S::kChunk, 1024), kIdescPV,
                              first && h == 0 ? 0u : 1u);
+                umma_commit_elected(h ? o_done(t) : o_half(t));
             }
-            umma_commit_elected(o_done(t));
             if (free_v) umma_commit_elected(v_empty(s));
             return true;
         };
@@ -736,14 +803,15 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const int qi = (kNarrow ? 0 : t * T) + ti;               // query within the item
         const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
         const uint32_t s_row = tmem_s(t) + lane_base, o_row = tmem_o(t) + lane_base;
-        const float sl = p.logit_scale_log2;
-        int cnt = 0, exchanges = 0;                              // the stream's KV tiles; rows handed over
+        int gj = 0, cnt = 0, exchanges = 0;                              // the stream's KV tiles; rows handed over
         bool ok = true;
         Cursor cu = start;
         Piece pc;
         while (ok && next_piece(cu, pc)) {
             const int n = pc.j1 - pc.j0;
             const int mine = kNarrow ? (n + 1 - t) >> 1 : n;     // KV tiles of this stream
+            const int g0 = gj + (kNarrow ? t : 0);               // the CTA's number of the stream's first tile
+            gj += n;
             if (mine == 0) continue;                             // a one-tile piece has no odd stream
             const bool valid = r < rows && qi < pc.nq;
             const bool idle = !__any_sync(0xffffffffu, valid);
@@ -760,69 +828,78 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tc_fence_after();
                 const int t0 = (pc.j0 + (kNarrow ? 2 * i + t : i)) * S::kKvTok;
                 const bool edge = t0 + S::kKvTok - 1 > first_pos;
-                // pass 1: the row's maximum, kCols columns at a time (loops, not unrolled code: see the conversion)
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const int g = g0 + (kNarrow ? 2 * i : i);
+                if (!(ok = wait_all(f_full(g % S::kFactorSlots), (g / S::kFactorSlots) & 1))) break;
+                // The tile's halves of 64 tokens, each a step of the online softmax on logits read once (a loop, not
+                // unrolled code: see the conversion), so that P V starts on the first while the second is worked
+                // on. The logits, the sums over the codes times the tokens' factors, are taken relative to the
+                // running maximum at once; where one lies above it by more than 8 (in the second half 15) the
+                // maximum is raised, and O and the sum are scaled, unless they are 0: in the second half the P V of
+                // the first has to be in O by then.
 #pragma unroll 1
-                for (int c = 0; c < 128; c += kCols) {
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t f = factors(g % S::kFactorSlots) + 4 * kCols * h;
+                    uint64_t v[16];
+                    load_factors(f, v);                          // (behind the logits' round trip)
                     float x[kCols];
-                    tmem_ld_cols(s_row + c, x);
-                    if (edge) mask_past(x, prow - t0 - c);
+                    tmem_ld_cols(s_row + kCols * h, x);
+                    const bool fresh = m_run == -INFINITY;       // the row has seen no position
+                    const float m_use = fresh ? 0.f : m_run;
+                    const uint64_t m2 = pack_f32x2(-m_use, -m_use);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    relative_logits(x, 0, v, m2);
+                    load_factors(f + 128, v);
+                    relative_logits(x, 32, v, m2);
+                    if (edge) mask_past(x, prow - t0 - kCols * h);   // (after the product: a factor may be 0)
 #pragma unroll
                     for (int e = 0; e < kCols / 2; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
-                }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-                const bool raise = mt > m_run + S::kRescaleThreshold;
-                const float m_new = raise ? mt : m_run;
-                // O_t is final for this tile: its last product completed before this S was issued
-                if (i > 0 && __any_sync(0xffffffffu, raise)) {
-                    const float alpha = raise ? fast_exp2(m_run - m_new) : 1.f;
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool raise = mt > (fresh ? -INFINITY : h ? S::kSecondThreshold : S::kRescaleThreshold);
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float up = raise ? mt : 0.f;
+                        const float alpha = raise ? fresh ? 0.f : fast_exp2(-mt) : 1.f;
+                        if (i + h > 0) {
+                            if (h && !(ok = wait_all(o_half(t), cnt & 1))) break;
+                            tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float o[32];
-                        tmem_ld32(o_row + 32 * c, o);
+                            for (int c = 0; c < 4; ++c) {
+                                float o[32];
+                                tmem_ld32(o_row + 32 * c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                        tmem_st32(o_row + 32 * c, o);
+                                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                tmem_st32(o_row + 32 * c, o);
+                            }
+                        }
+                        l_run *= alpha;
+                        if (raise) m_run = m_use + mt;
+                        const uint64_t up2 = pack_f32x2(-up, -up);
+#pragma unroll
+                        for (int e = 0; e < kCols; e += 2)
+                            unpack_f32x2(add_f32x2(pack_f32x2(x[e], x[e + 1]), up2), x[e], x[e + 1]);
                     }
-                    l_run *= alpha;
-                }
-                m_run = m_new;
-                const float m_use = fmaxf(m_run, kLogitFloor);   // (a row that has seen nothing: all weights 0)
-                // pass 2: probabilities exp2(s * sl - m) to f16 for the products, and to the row sum before that
-                // rounding (its errors, half a step each, average out over the row), two at a time
-                const uint64_t sl2 = pack_f32x2(sl, sl), m2 = pack_f32x2(-m_use, -m_use);
-                uint64_t sum0 = 0, sum1 = 0;                     // two packed partial sums each
-#pragma unroll 1
-                for (int c = 0; c < 128; c += kCols) {
-                    float x[kCols];
-                    tmem_ld_cols(s_row + c, x);
-                    if (edge) mask_past(x, prow - t0 - c);
+                    // probabilities exp2 of that to f16 for the products, and to the row sum before that rounding
+                    // (its errors, half a step each, average out over the row), two at a time
+                    uint64_t sum0 = 0, sum1 = 0;                 // two packed partial sums each
 #pragma unroll
                     for (int q = 0; q < kCols; q += 32) {
                         float w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float y0, y1;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(x[q + 2 * e], x[q + 2 * e + 1]), sl2, m2), y0, y1);
-                            y0 = fast_exp2(y0);
-                            y1 = fast_exp2(y1);
+                            const float y0 = fast_exp2(x[q + 2 * e]), y1 = fast_exp2(x[q + 2 * e + 1]);
                             if (e & 1) sum1 = add_f32x2(sum1, pack_f32x2(y0, y1));
                             else sum0 = add_f32x2(sum0, pack_f32x2(y0, y1));
                             w[e] = __uint_as_float(pack_half2(y0, y1));
                         }
-                        tmem_st16(s_row + (c + q) / 2, w);       // P over logits already read
+                        tmem_st16(s_row + (kCols * h + q) / 2, w);   // P over logits already read
                     }
-                    if ((c + kCols) % 64 == 0) {                 // a half of P is in place (and O rescaled)
-                        tmem_wait_st();
-                        tc_fence_before();
-                        mbar_arrive(p_full(t, c >> 6));
-                    }
-                }
-                {
                     float u0, u1;
                     unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
                     l_run += u0 + u1;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full(t, h));
                 }
+                if (!ok) break;
             }
             if (!ok) break;
             if (!(ok = wait_all(o_done(t), (cnt - 1) & 1))) break;

@@ -1539,9 +1539,7 @@ pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void
     prm.max_blocks_per_seq = max_blocks_per_seq;
     prm.num_blocks = num_blocks;
     prm.max_context_len = max_context_len;
-    const float scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
-    prm.logit_scale_log2 = scale_log2 > 0.f ? scale_log2 : 1.f;
-    prm.key_sign = scale_log2 > 0.f ? (softmax_scale < 0.f ? -1.f : 1.f) : 0.f;
+    prm.logit_scale_log2 = softmax_scale * 1.4426950408889634f;
     return launch_chunk_int8(prm, q, k_cache, v_cache, kv_scales, workspace, workspace_bytes, st);
 }
 

@@ -65,14 +65,13 @@ def attention(q, codes_k, codes_v, scales, tables, lens, query_start, softmax_sc
     on what a kernel may be off, from its roundings:
       * weights rounded to f16 (half a step), the f16 output (half a step), and, in the matrix-product
         form, values rounded to f16 (half a step): 3 half steps of sum p |v|, one of |out|;
-      * logits: keys rounded to f16 (half a step of every term) and fp32 sums of 128 terms, fp32
-        exp2/log2 (2^-21) and the fp32 rounding of the logit itself: a weight is off by exp(d), its
-        normalised value by at most exp(2 d);
+      * logits: fp32 sums of 128 exact terms, fp32 exp2/log2 (2^-21) and the fp32 roundings of the
+        logit itself (its scale, the product, the difference to the maximum): a weight is off by
+        exp(d), its normalised value by at most exp(2 d);
       * weights below the normal f16 range are off by 2^-25 of the largest;
-      * values and keys below it are staged off by half a subnormal step, 2^-25 each: that much of sum p = 1
-        for the values, softmax_scale sum |q| times it for a logit. (A small row's value is rounded at a
-        normal magnitude first, half a step, which is the 2^-11 counted above, and then to the subnormal
-        one: the two add.)"""
+      * values below it are staged off by half a subnormal step, 2^-25: that much of sum p = 1. (A small
+        row's value is rounded at a normal magnitude first, half a step, which is the 2^-11 counted
+        above, and then to the subnormal one: the two add.)"""
     B = len(lens)
     Hq, G = q.shape[1], q.shape[1] // codes_k.shape[2]
     out, bound = np.zeros(q.shape, F64), np.zeros(q.shape, F64)
@@ -101,8 +100,7 @@ def attention(q, codes_k, codes_v, scales, tables, lens, query_start, softmax_sc
             p /= p.sum(-1, keepdims=True)
             out[r0:r1, h] = p @ V[:, g]
             absum = p @ np.abs(V[:, g])
-            d = np.where(hidden, 0, mag * (HALF + 130 * 2.0 ** -24)).max(-1) + 2.0 ** -20 \
-                + 2.0 ** -25 * abs(softmax_scale) * np.abs(qq).sum(-1) \
+            d = np.where(hidden, 0, mag * (130 * 2.0 ** -24)).max(-1) + 2.0 ** -20 \
                 + np.where(hidden, 0, np.abs(x) + 64).max(-1) * 2.0 ** -22
             small = 2.0 ** -25 * (np.where(hidden, 0, 1.0) @ cv[:, g]) * vs[:, g].max()
             bound[r0:r1, h] = (3.1 * HALF + np.expm1(2 * d))[:, None] * absum + HALF * np.abs(out[r0:r1, h]) \

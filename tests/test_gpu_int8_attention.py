@@ -350,6 +350,18 @@ def test_chunk_many_sequences_and_ragged_items():
     c.check(c.chunk(), "many sequences, wide")
 
 
+@pytest.mark.parametrize("B,n,hi", [(64, 5, 2048), (96, 3, 700), (148, 9, 260), (24, 40, 1500)])
+def test_chunk_runs_of_many_pieces(B, n, hi):
+    """Several items per CTA, of one KV tile to many, so that stages and barriers run on across pieces."""
+    rng = np.random.default_rng(B)
+    c = Case(300 + B, 14, 2, list(rng.integers(n, hi, B)), [n] * B)
+    ws = workspace()
+    got = c.chunk(ws)
+    c.check(got, f"{B} sequences")
+    assert np.array_equal(got, c.chunk(ws))
+    assert pkv.pkv_device_error() == 0
+
+
 # ------------------------------------------------------------------ how calls meet
 def test_one_workspace_serves_every_plan_in_turn():
     ws = workspace()
