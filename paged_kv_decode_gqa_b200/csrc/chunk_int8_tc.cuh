@@ -62,7 +62,8 @@
 // Against 164 / 56 of the present form: the waits' slow path inlined 176 / 65;
 // registers moved to the softmax (setmaxnreg, inlined waits) 170 / 63; the scales
 // brought in by a warp of their own 195 / 71; four warps each for K and V 183 / 67;
-// the conversion rolled up to 16 channels 174 / 63.
+// the conversion rolled up to 16 channels 174 / 63; double-buffered halves with an
+// issuing warp per stream 162 / 57 (timed in turn: no difference).
 #pragma once
 
 #include "int8_cache.cuh"
