@@ -362,6 +362,15 @@ def test_chunk_runs_of_many_pieces(B, n, hi):
     assert pkv.pkv_device_error() == 0
 
 
+@pytest.mark.parametrize("news", [None, [5, 4, 3], [40, 33, 130]])
+def test_sequences_that_share_pages(news):
+    """A common prefix: three tables name the same pages for the first 160 tokens."""
+    c = Case(77, 14, 2, [300, 190, 420], news)
+    for b in (1, 2):
+        c.tables[b, :10] = c.tables[0, :10]
+    c.check(c.decode() if news is None else c.chunk(), "shared prefix")
+
+
 # ------------------------------------------------------------------ how calls meet
 def test_one_workspace_serves_every_plan_in_turn():
     ws = workspace()
