@@ -1002,7 +1002,10 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             if (valid) __stcg(reinterpret_cast<float2*>(part + 128 * 128 * 4) + r, make_float2(m_run, l_run));
             release_o();
-            if constexpr (kNarrow) continue;                     // merged at the CTA's end
+            if constexpr (kNarrow) {                             // merged at the CTA's end, by bulk copies
+                fence_proxy_async_global();
+                continue;
+            }
             // Wide: the warp's ticket for its 32 rows. The warp barrier orders every lane's stores before lane
             // 0's release-acquire; the loads of the last one, which merges, follow its acquire:
             // out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of the pieces, whoever merges.
@@ -1062,7 +1065,8 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // item's last ticket merges its pieces, all threads together, through the shared memory that is free by now,
     // three pieces at a time by bulk copy. (Merged warp by warp as above, 4 tokens on one 2000-token context took
     // 28 us instead of 18.) The block's barrier orders the pieces' stores before the release-acquire ticket; the
-    // copies behind its acquire come after the next barrier. ----
+    // copies behind its acquire come after the next barrier. The stores are the generic proxy's and the copies the
+    // async proxy's: a proxy fence follows the stores, and another precedes the copies. ----
     const int n_cut = *s_cuts;
     if (n_cut == 0) return;
     if (warp < n_cut && lane == 0) {                             // an item is known by the last CTA it reaches
@@ -1097,6 +1101,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             auto piece_at = [&](int u) { return part_of(c0 + u, c0 + u == c_first ? first_slot : 0, 0); };
             if (threadIdx.x == 0) {
                 fence_proxy_async_shared();
+                fence_proxy_async_global();
                 mbar_arrive_expect_tx(merge_bar, (uint32_t)(n_new * 512 * lp));
                 for (int u = 0; u < n_new; ++u)
                     bulk_load(base + (uint32_t)(s0 + u) * 65536u, piece_at(u), (uint32_t)(512 * lp), merge_bar);

@@ -113,6 +113,12 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Orders generic-proxy accesses to global memory with async-proxy ones (bulk copies) on both sides of it. A
+// barrier, an atomic's release or acquire and the fence above order nothing between the two proxies there.
+__device__ __forceinline__ void fence_proxy_async_global() {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // 16-byte global load of data read once (no L1 allocation).
 __device__ __forceinline__ uint4 ld_stream_16(const uint4* src) {
     uint4 v;
