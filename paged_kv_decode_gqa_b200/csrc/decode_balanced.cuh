@@ -385,6 +385,7 @@ decode_balanced_kernel(const __grid_constant__ CUtensorMap tm_k,
             unsigned int prev = 0;
             if (lane == 0) prev = atomic_add_acq_rel_gpu(cnt, 1u);
             prev = __shfl_sync(0xffffffffu, prev, 0);
+            __syncwarp();                           // the acquire is lane 0's: the shuffle orders no memory
             if (prev != (unsigned int)(last - first)) return;   // another item merges the group
             // ---- merge items first..last ----
             // (m, l) are loaded lane-parallel. The items' values come either

@@ -639,6 +639,7 @@ stream_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         unsigned int prev = 0;
         if (lane == 0) prev = atomic_add_acq_rel_gpu(cnt, 1u);
         prev = __shfl_sync(0xffffffffu, prev, 0);
+        __syncwarp();                           // the acquire is lane 0's: the shuffle orders no memory
         if (prev != (unsigned int)(last - first)) {             // another item merges the node
             leave_ring();
             return;

@@ -7,6 +7,8 @@ to every kind of access that takes part.
 import pathlib
 import re
 
+import pytest
+
 CSRC = pathlib.Path(__file__).resolve().parents[1] / "paged_kv_decode_gqa_b200" / "csrc"
 
 
@@ -27,3 +29,14 @@ def test_pieces_read_by_bulk_copies_are_fenced_between_the_proxies():
     assert barrier < ticket
     assert "fence_proxy_async_global()" in text[stores:barrier]
     assert "fence_proxy_async_global()" in text[ticket:copy]
+
+
+@pytest.mark.parametrize("name", ["stream_int8.cuh", "chunk_int8_tc.cuh", "decode_balanced.cuh", "prefill_tc.cuh"])
+def test_a_warps_ticket_is_followed_by_a_warp_barrier(name):
+    """Lane 0 takes a warp's ticket and tells the others by a shuffle, which orders no memory: a warp barrier
+    follows, before any lane reads what the ticket's acquire makes visible."""
+    text = _code(name)
+    tickets = [m.end() for m in re.finditer(r"prev = __shfl_sync\(0xffffffffu, prev, 0\);", text)]
+    assert tickets
+    for end in tickets:
+        assert re.match(r"\s*__syncwarp\(\);", text[end:]), text[end:end + 120]
