@@ -646,9 +646,10 @@ pkv_status paged_gqa_decode_attention_int8(void* out, const void* q, const void*
  * `workspace` (paged_gqa_prefill_workspace_size(..., PKV_KV_INT8) bytes) is
  * required, with the rules of paged_gqa_decode_attention_int8. Chunks of more
  * than 8 (query token, head of a KV head) pairs run on the tensor cores with
- * the cached values (V) rounded to f16 (magnitudes past its range saturate); the
- * keys enter as their codes, their scales in fp32. Sequences
- * with inconsistent lengths are flagged and their rows left alone.
+ * the cached values (V) rounded to f16, to half a step of the value whatever its
+ * scale, or to 2^-32 of the largest V scale of its 64 tokens where that is more;
+ * the keys enter as their codes, their scales in fp32. Sequences with
+ * inconsistent lengths are flagged and their rows left alone.
  */
 pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
                                             const float* kv_scales,

@@ -5,11 +5,19 @@
 // attends causally to positions [0, p] of the sequence's 8-bit cache
 // (int8_cache.cuh), query head h reading KV head h / G. A key enters the
 // products as its codes less 128, exact in f16, and its scale as a factor of
-// the logit in fp32. A cached value is (code - 128) * scale, rounded to f16 as
-// it is staged for the tensor cores (half a step, 2^-11; values past the f16
-// range saturate). (With the keys rounded to f16 as well the output's error
-// was 0.00032 of its norm, where f16 outputs alone are off by 0.00019; it is
-// 0.00025 so, at nearly the same speed.)
+// the logit in fp32. A cached value is (code - 128) * scale. It is staged for
+// the tensor cores as (code - 128) * scale * 2^-e, rounded to f16 (half a step,
+// 2^-11), with e of its half of the KV tile chosen by the half's largest scale
+// (value_exponent): whatever the scales, no value leaves the f16 range, and
+// one is below its normal part only where it is 2^-21 of the half's largest scale.
+// The weights make up for it: 2^(x + e - m) for a token of logit x, m being the
+// row's running maximum of x + e, and the row's sum takes them times 2^-e. (With
+// the keys rounded to f16 as well the output's error was 0.00032 of its norm,
+// where f16 outputs alone are off by 0.00019; it is 0.00025 so, at nearly the
+// same speed. With the values as exact codes too, their scales multiplied into the
+// weights, it was 0.00021, but 210 and 68 us instead of 174 and 59 for the two cases
+// below: the second factor per token doubles the reads of factors by every
+// softmax thread.)
 //
 // Structure (one CTA per SM, persistent):
 //  * A query tile is T = floor(128 / G) query tokens x the G heads of one KV
@@ -32,8 +40,8 @@
 //  * Staging: one TMA warp brings the codes of K (128-byte swizzle), the scales
 //    and Q, one the codes of V; four warps convert them, one token (row) per
 //    thread: a code becomes an exact f16 integer (a byte permute and a
-//    subtraction), and for V, whose scale is thus a register, code * scale is
-//    formed in f16x2 as code * hi + (code * lo) with scale = hi + lo split into
+//    subtraction), and for V, whose scale (times 2^-e) is thus a register, code * scale
+//    is formed in f16x2 as code * hi + (code * lo) with scale = hi + lo split into
 //    two f16, so that the scale's own rounding does not add to the value's
 //    (RowScale). The f16 tiles are written in the 128-byte swizzled layout the
 //    tensor cores read: K and V are double-buffered. Codes are finite and rows
@@ -93,7 +101,7 @@ struct ChunkInt8Shape {
     static constexpr int kRaw = 128 * 128;              // codes of K or V of a KV tile
     static constexpr int kScales = 8 * 128;             // scales of a KV tile: 8 pages x (16 K, 16 V)
     static constexpr int kBarBytes = 320;
-    static constexpr int kFactors = 128 * 4;            // logit factors of a KV tile's tokens
+    static constexpr int kFactors = 128 * 4 + 2 * 8;    // logit factors of a KV tile's tokens; e, 2^-e of its halves
     static constexpr int kFactorSlots = 3;
     // Q A | Q B or a second raw stage | K x 2 | V x 2 | raw K, V | scales | factors x 3 | barriers and words.
     static constexpr int kOffQ = 0;
@@ -115,6 +123,14 @@ struct ChunkInt8Shape {
     static constexpr float kRescaleThreshold = 8.f, kSecondThreshold = 15.f;
     static constexpr int kPartBytes = 128 * 128 * 4 + 128 * 8;
 };
+
+// The power of two that the V scales of half a KV tile (64 tokens; `most` the largest) are brought to f16 by:
+// scale * 2^-e is below 2^8, so that no code takes it past the f16 range, and the largest at least 2^7 unless e is
+// at its least. (Rows of scales below 2^-33 are zeros in any f16 output.)
+__device__ __forceinline__ int value_exponent(float most) {
+    return max((int)((__float_as_uint(most) >> 23) & 0xff) - 127 - 7, -40);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // A token's scale for the conversion: scale = (hi + lo) * post, hi and lo f16. post is 1 unless the
 // scale is small (below 2^-10, where lo would lose bits to the subnormal range): then hi + lo is the
@@ -654,18 +670,17 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
             }
         };
-        // the row's scale: 0 past the context; outside [0, 2^60] flagged and 0
-        auto row_scale = [&](const Piece& pc, int j, uint32_t addr) -> float {
-            const float s = lds32(addr);
-            const bool live = j * S::kKvTok + row < min(pc.L, pc.npages * kPageRows);
+        // the scale of KV tile j's row r (`which` 0: K, 64: V): 0 past the context; outside [0, 2^60] flagged and 0
+        auto row_scale = [&](const Piece& pc, int j, int r, uint32_t which) -> float {
+            const float s = lds32(raw_sc + (uint32_t)((r >> 4) * 128 + (r & 15) * 4) + which);
+            const bool live = j * S::kKvTok + r < min(pc.L, pc.npages * kPageRows);
             const bool fine = s >= 0.f && s <= kScaleMax;
             if (live && !fine) flag_error(PKV_DEVERR_SCALE);
             return live && fine ? s : 0.f;
         };
-        const uint32_t sc_off = (uint32_t)((row >> 4) * 128 + (row & 15) * 4);
         // stages the K (with its tokens' logit factors) or V of KV tile g, the piece's `first` or not; false when a
         // wait ran out
-        auto stage_tile = [&](bool is_k, int g, bool first, float scale) -> bool {
+        auto stage_tile = [&](bool is_k, int g, bool first, float scale, int exponent) -> bool {
             const int s = g % kRawStages, d = g & 1;
             if (!wait_all(is_k ? rk_full(s) : rv_full(s), (g / kRawStages) & 1)) return false;
             if (g >= 2 && !wait_all(is_k ? k_empty(d) : v_empty(d), ((g >> 1) - 1) & 1)) return false;
@@ -676,6 +691,10 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (kNarrow && !first && g >= 3 && !wait_all(v_empty(d ^ 1), ((g - 3) >> 1) & 1)) return false;
                 const int slot = g % S::kFactorSlots;
                 asm volatile("st.shared.f32 [%0], %1;" :: "r"(factors(slot) + 4 * row), "f"(scale) : "memory");
+                if ((row & 63) == 0)
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};"
+                                 :: "r"(factors(slot) + 512 + (row >> 3)), "f"((float)exponent), "f"(power_of_two(-exponent))
+                                 : "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(f_full(slot));
             }
@@ -695,20 +714,24 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         while (ok && next_piece(cu, pc)) {
             const int n = pc.j1 - pc.j0;
             // K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
-            float v_scale = 0.f, v_next = 0.f;
+            float v_scale = 0.f, v_next = 0.f;                     // in units of their half's 2^e
             for (int step = 0; step < 2 * n; ++step) {
                 const bool is_k = step < 2 * n - 1 && (step == 0 || (step & 1));
                 const int i = is_k ? (step + 1) >> 1 : step == 2 * n - 1 ? n - 1 : (step >> 1) - 1;
                 float scale = v_scale;
+                int exponent = 0;
                 if (is_k) {
                     if (!(ok = wait_all(rs_full, (gj + i) & 1))) break;
-                    scale = row_scale(pc, pc.j0 + i, raw_sc + sc_off) * p.logit_scale_log2;
-                    v_next = fminf(row_scale(pc, pc.j0 + i, raw_sc + sc_off + 64), 511.75f);   // at the f16 range
+                    scale = row_scale(pc, pc.j0 + i, row, 0) * p.logit_scale_log2;
+                    v_next = row_scale(pc, pc.j0 + i, row, 64);
+                    // (the half's other 32 tokens are another warp's: both come to the same exponent)
+                    exponent = value_exponent(warp_max(fmaxf(v_next, row_scale(pc, pc.j0 + i, row ^ 32, 64))));
+                    v_next *= power_of_two(-exponent);
                     if (i == 0) v_scale = v_next;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(rs_empty);
                 }
-                if (!(ok = stage_tile(is_k, gj + i, i == 0, scale))) break;
+                if (!(ok = stage_tile(is_k, gj + i, i == 0, scale, exponent))) break;
                 if (!is_k) v_scale = v_next;
             }
             gj += n;
@@ -833,20 +856,24 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (!(ok = wait_all(f_full(g % S::kFactorSlots), (g / S::kFactorSlots) & 1))) break;
                 // The tile's halves of 64 tokens, each a step of the online softmax on logits read once (a loop, not
                 // unrolled code: see the conversion), so that P V starts on the first while the second is worked
-                // on. The logits, the sums over the codes times the tokens' factors, are taken relative to the
-                // running maximum at once; where one lies above it by more than 8 (in the second half 15) the
-                // maximum is raised, and O and the sum are scaled, unless they are 0: in the second half the P V of
-                // the first has to be in O by then.
+                // on. The logits, the sums over the codes times the tokens' factors, plus the half's e, are taken
+                // relative to the running maximum at once; where one lies above it by more than 8 (in the second half
+                // 15) the maximum is raised, and O and the sum are scaled, unless they are 0: in the second half the
+                // P V of the first has to be in O by then.
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t f = factors(g % S::kFactorSlots) + 4 * kCols * h;
+                    // e and 2^-e of the half's V scales (before the logits: read behind them, e costs 100 bytes of spills)
+                    const uint32_t ex = factors(g % S::kFactorSlots) + 512 + 8 * h;
+                    const float e_half = lds32(ex);
                     uint64_t v[16];
                     load_factors(f, v);                          // (behind the logits' round trip)
                     float x[kCols];
                     tmem_ld_cols(s_row + kCols * h, x);
                     const bool fresh = m_run == -INFINITY;       // the row has seen no position
                     const float m_use = fresh ? 0.f : m_run;
-                    const uint64_t m2 = pack_f32x2(-m_use, -m_use);
+                    const float e_less_m = e_half - m_use;
+                    const uint64_t m2 = pack_f32x2(e_less_m, e_less_m);
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     relative_logits(x, 0, v, m2);
                     load_factors(f + 128, v);
@@ -895,7 +922,7 @@ chunk_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                     float u0, u1;
                     unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
-                    l_run += u0 + u1;
+                    l_run = fmaf(u0 + u1, lds32(ex + 4), l_run);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(p_full(t, h));
