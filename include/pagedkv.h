@@ -579,8 +579,9 @@ pkv_status paged_kv_cache_read(void* k_out, void* v_out, const void* k_cache, co
  *             axis_sections[1] to axis 1, ...;
  *   cyclic:   j belongs to axis a = j mod num_axes when a > 0 and
  *             j < num_axes * axis_sections[a], else to axis 0.
- * Angles are formed in fp64 and reduced before the sine and cosine, so
- * positions as far as 2^31 keep fp32 accuracy. The rotation is fp32 and is
+ * Angles are reduced in fp64 with the products' low parts kept, before the
+ * sine and cosine, so positions as far as 2^53, of either sign, keep fp32
+ * accuracy: a reduced angle is off by its rounding to fp32. The rotation is fp32 and is
  * rounded once, to the f16 of q_out or to the cache's type (an 8-bit or FP8
  * cache quantises the unrounded fp32 values).
  *

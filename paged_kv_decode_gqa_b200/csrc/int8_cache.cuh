@@ -18,10 +18,11 @@
 // and every thread keeps the eight it needs in registers for all its rows. No
 // block-wide step exists. A token's rows are shared out over several warps only
 // when there are too few tokens to fill the SMs.
-// Angles: pos * inv_freq in fp64 (exact: 24 significant bits times an integer
-// below 2^29, and within 2^-53 past it), reduced to a fraction of a turn, then
-// the fp32 sincospi. In fp32 a position near 2^20 would leave the fastest angle
-// off by 2^-4 radians.
+// Angles: a fraction of a turn, from fp64 arithmetic in which the product of the
+// position and the frequency and that with 1 / (2 pi) keep their low parts
+// (turn_fraction), then the fp32 sincospi. In fp32 a position near 2^20 would
+// leave the fastest angle off by 2^-4 radians; in plain fp64 one near 2^31 by
+// 4e-7, several times the rounding of the reduced angle to fp32.
 // Rounding: fp32 throughout, once to f16, to E4M3 (of x / scale, an IEEE
 // division, as paged_kv_cache_write) or to the 8-bit code.
 // Bound: HBM; every row is read and written once. Measured at 28 / 4 heads: f16,
@@ -164,6 +165,16 @@ __device__ __forceinline__ uint2 quantize8_int8(const float (&f)[8], float scale
                       prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u));
 }
 
+// pos * freq / (2 pi) less the nearest integer, to 2^-52 for |pos| up to 2^53 (a position past that is rounded to
+// fp64 first). With c + c' = 1 / (2 pi) to 2^-109: the product a + a' is exact (multiply-adds keep what a product
+// rounds off), t = a c has its low part kept as well, and t less its integer part is exact.
+__device__ __forceinline__ double turn_fraction(double pos, double freq) {
+    constexpr double c = 0.15915494309189535, c_low = -9.839338337591243e-18;
+    const double a = pos * freq, a_low = fma(pos, freq, -a);
+    const double t = a * c;
+    return (t - rint(t)) + (fma(a, c, -t) + fma(a, c_low, a_low * c));
+}
+
 // Position axis of frequency j.
 __device__ __forceinline__ int rope_axis(const RopeWriteParams& p, int j) {
     if (p.cyclic) {
@@ -253,14 +264,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const
     };
 #pragma unroll
     for (int u = 0; u < kRopeBatch; ++u) load(u, tok, 4 * split + u * stride + sub);
-    // this lane's frequencies, in turns per position, and their axes
+    // this lane's frequencies and their axes
     double freq[2] = {0.0, 0.0};
     const int64_t* where[2] = {p.positions, p.positions};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int j = lane + 32 * e;
         if (j < p.half) {
-            freq[e] = (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
+            freq[e] = (double)__ldg(p.inv_freq + j);
             where[e] += (int64_t)rope_axis(p, j) * p.num_tokens;
         }
     }
@@ -273,8 +284,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_cache_write_kernel(const
         for (int e = 0; e < 2; ++e) {
             const int j = lane + 32 * e;
             if (j < p.half) {
-                const double turns = (double)pos[e] * freq[e];
-                const float frac = (float)(turns - rint(turns));     // in [-1/2, 1/2]
+                const float frac = (float)turn_fraction((double)pos[e], freq[e]);     // in [-1/2, 1/2]
                 sincospif(2.f * frac, &turn[j].y, &turn[j].x);
             }
         }
