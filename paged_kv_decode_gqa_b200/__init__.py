@@ -443,21 +443,22 @@ def paged_gqa_prefill_attention(out, q, k_cache, v_cache, block_tables, context_
 # tensors and the call itself are native (csrc/binding.cpp). A tensor must be dense, of its type and
 # shape, and on the current device, whose current stream is the default.
 
-BINDING_PATH = os.path.join(_HERE, "_binding.so")
 _binding = None
 
 
 def _load_binding():
-    """The CPython binding, loaded on first use and bound to the CUDA library's functions."""
+    """The CPython binding of this Python and PyTorch, loaded on first use and bound to the CUDA library's functions."""
     global _binding
     import importlib.machinery
     import importlib.util
     import torch  # noqa: F401  (the binding's symbols come from it)
-    if not os.path.exists(BINDING_PATH):
-        raise ImportError(f"binding not built: {BINDING_PATH} is missing "
+    from .build import binding_path
+    path = binding_path()
+    if not os.path.exists(path):
+        raise ImportError(f"binding not built: {path} is missing "
                           "(run `python -m paged_kv_decode_gqa_b200.build`)")
     lib = load_library()
-    loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+    loader = importlib.machinery.ExtensionFileLoader("_binding", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
