@@ -546,9 +546,10 @@ pkv_status paged_kv_cache_write_int8(const void* k_new, const void* v_new,
                                      int32_t num_blocks, int32_t block_size, void* stream);
 
 /*
- * paged_kv_cache_read -- the inverse of the writes, for every cache type:
- * k_out[i], v_out[i] ([T, Hkv, 128] f16) are the values of slot
- * slot_mapping[i]: f16 copied; FP8 decoded * k_scale (v_scale); 8-bit
+ * paged_kv_cache_read -- the inverse of the writes: k_out[i], v_out[i] ([T,
+ * Hkv, 128] f16) are the values of slot slot_mapping[i]: f16 copied; FP8
+ * decoded * k_scale (v_scale), one number for the cache (a cache written with
+ * device-side scales, the *_fp8_scaled calls, has no read of its own); 8-bit
  * (code - 128) * scale; the products in fp32, rounded once to f16. A slot may
  * be read more than once. Negative slots leave their rows of the outputs as
  * they were; so do slots outside the pool, which are flagged. kv_scales is

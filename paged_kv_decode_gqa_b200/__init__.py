@@ -488,7 +488,8 @@ def paged_kv_cache_write_int8(k_new, v_new, k_cache, v_cache, kv_scales, slot_ma
 def paged_kv_cache_read(k_out, v_out, k_cache, v_cache, slot_mapping, *, kv_dtype="f16", kv_scales=None,
                         k_scale=1.0, v_scale=1.0, stream=None) -> None:
     """k_out[i], v_out[i] ([T, Hkv, D] float16) = the cached values of slot slot_mapping[i], for an
-    "f16", "fp8" or "int8" cache. Rows of negative slots are left as they were."""
+    "f16", "fp8" or "int8" cache. Rows of negative slots are left as they were. The scales of an "fp8" cache
+    are numbers, one for the cache (CUDA tensors are refused: reading them would wait for the stream)."""
     status = (_binding or _load_binding()).cache_read(k_out, v_out, k_cache, v_cache, slot_mapping,
                                                       _cache_dtype_code(kv_dtype), kv_scales, k_scale, v_scale, stream)
     if status:
@@ -504,8 +505,8 @@ def paged_kv_rope_cache_write(q_out, q, k_new, v_new, k_cache, v_cache, slot_map
     positions [T] or [axes, T] int64; inv_freq [rotary_dim / 2] float32 (rotary_dim a multiple of 16,
     channels past it are left as they are). `sections`: frequencies per axis (default: one axis), in
     runs, or round the axes (cyclic_axes). `interleaved`: channels (2j, 2j + 1) form a pair, else
-    (j, j + rotary_dim / 2). For an "fp8" cache k_scale and v_scale are numbers, or float32 CUDA
-    tensors of 1 or Hkv elements.
+    (j, j + rotary_dim / 2). For an "fp8" cache k_scale and v_scale are both numbers, or both float32
+    CUDA tensors of 1 or Hkv elements.
     """
     flags = (PKV_ROPE_INTERLEAVED if interleaved else 0) | (PKV_ROPE_CYCLIC_AXES if cyclic_axes else 0)
     status = (_binding or _load_binding()).rope_cache_write(

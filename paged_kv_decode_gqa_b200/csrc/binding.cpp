@@ -120,6 +120,14 @@ float number(PyObject* o) {
     return (float)v;
 }
 
+// A scale of the whole cache. Not a CUDA tensor: its value would have to be copied to the host first, which waits
+// for the stream and cannot be captured.
+float scale_number(PyObject* o, const char* name) {
+    if (THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda())
+        raise(PyExc_TypeError, std::string(name) + " must be a number here, not a CUDA tensor");
+    return number(o);
+}
+
 // A paged cache of any type.
 struct Cache {
     void *k, *v;
@@ -200,7 +208,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t T = int32(slots.numel(), "slot_mapping");
         void* k = c.take(a[0], "k_out", at::kHalf, {T, cache.heads, cache.dim});
         void* v = c.take(a[1], "v_out", at::kHalf, {T, cache.heads, cache.dim});
-        const float ks = number(a[7]), vs = number(a[8]);
+        const float ks = scale_number(a[7], "k_scale"), vs = scale_number(a[8], "v_scale");
         void* st = c.stream(a[9]);
         return unlocked([&] {
             return g_lib.read(k, v, cache.k, cache.v, cache.scales, sm, T, cache.heads, cache.dim, cache.blocks, cache.rows,
@@ -269,7 +277,7 @@ PyObject* rope_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                              2 * half, axes, sections, cache.blocks, cache.rows, ks, vs, per_head, flags, st);
             });
         }
-        const float ks = number(a[13]), vs = number(a[14]);
+        const float ks = scale_number(a[13], "k_scale"), vs = scale_number(a[14], "v_scale");
         return unlocked([&] {
             return g_lib.rope(qo, qi, k, v, cache.k, cache.v, cache.scales, sm, ps, fr, T, Hq, cache.heads, cache.dim,
                               2 * half, axes, sections, cache.blocks, cache.rows, code, ks, vs, flags, st);
