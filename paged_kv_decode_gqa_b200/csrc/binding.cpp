@@ -92,7 +92,11 @@ struct Call {
     // None: the current stream; else an integer handle or an object with cuda_stream.
     void* stream(PyObject* o) const {
         if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device()).stream();
-        if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
+        if (PyLong_Check(o)) {
+            void* p = PyLong_AsVoidPtr(o);
+            if (!p && PyErr_Occurred()) throw Raised{};          // an integer that is no address
+            return p;
+        }
         PyObject* handle = PyObject_GetAttrString(o, "cuda_stream");
         if (!handle) throw Raised{};
         void* p = PyLong_AsVoidPtr(handle);

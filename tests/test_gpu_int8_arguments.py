@@ -66,3 +66,13 @@ def test_the_read_is_captured_without_a_copy_of_its_scales(call):
     graph.replay()
     torch.cuda.synchronize()
     assert (call["k"] == 0.5).all()
+
+
+def test_an_integer_that_is_no_stream_is_refused(call):
+    call["k"].fill_(3)
+    with pytest.raises(OverflowError):
+        read(call, "f16", stream=1 << 70)
+    torch.cuda.synchronize()
+    assert (call["k"] == 3).all()                                  # nothing ran on another stream
+    read(call, "f16", stream=torch.cuda.current_stream().cuda_stream)
+    assert (call["k"] == 0).all()
