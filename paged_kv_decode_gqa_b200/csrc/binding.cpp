@@ -251,7 +251,9 @@ PyObject* rope_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
             const Py_ssize_t len = PySequence_Fast_GET_SIZE(s);
             bool bad = len != axes || len > 16;
             for (Py_ssize_t i = 0; !bad && i < len; ++i) {
-                const long v = PyLong_Check(PySequence_Fast_GET_ITEM(s, i)) ? PyLong_AsLong(PySequence_Fast_GET_ITEM(s, i)) : -1;
+                PyObject* count = PyNumber_Index(PySequence_Fast_GET_ITEM(s, i));    // (NumPy's integers too)
+                const long v = count ? PyLong_AsLong(count) : -1;
+                Py_XDECREF(count);
                 bad = v < 0 || v > half;
                 sections[i] = (int32_t)v;
             }

@@ -76,3 +76,12 @@ def test_an_integer_that_is_no_stream_is_refused(call):
     assert (call["k"] == 3).all()                                  # nothing ran on another stream
     read(call, "f16", stream=torch.cuda.current_stream().cuda_stream)
     assert (call["k"] == 0).all()
+
+
+@pytest.mark.parametrize("of", [list, tuple, np.array, lambda x: [np.int32(v) for v in x], torch.tensor])
+def test_sections_are_any_integers(call, of):
+    call["pos"] = torch.zeros((2, 4), dtype=torch.int64, device="cuda")
+    rope(call, "f16", sections=of([40, 24]))
+    for bad in ([40, 25], [40.0, 24.0], [64], [65, -1], ["40", "24"]):
+        with pytest.raises((ValueError, pkv.PagedKVError)):
+            rope(call, "f16", sections=bad)
