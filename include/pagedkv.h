@@ -195,7 +195,13 @@ int32_t paged_gqa_decode_suggest_partition(int32_t batch, int32_t num_kv_heads,
  *   once and reused. A call that ended with a barrier-wait timeout
  *   (PKV_DEVERR_WAIT_TIMEOUT) can leave counters set: zero-fill the
  *   workspace again before reusing it. Calls that share a workspace must not
- *   run concurrently on different streams.
+ *   run concurrently on different streams. The counters' place depends on the
+ *   kind of call: PKV_PARTITION_AUTO and the decode steps of one cache type
+ *   keep one place, fixed partitions one per (batch, heads, partitions),
+ *   paged_gqa_prefill_attention its own, the *_int8 calls theirs. Between
+ *   calls of different kinds a workspace must be zero-filled again, or each
+ *   kind given its own: what one leaves in another's counters goes unnoticed
+ *   and loses pieces of the result.
  *
  * max_context_len must be >= every context_lens[b] (larger lengths are
  * clamped and flagged) and <= max_blocks_per_seq * block_size.
@@ -628,7 +634,8 @@ size_t paged_gqa_decode_workspace_size_int8(void);
  * ready for the next call, as there; calls that share one must not run
  * concurrently (two captured graphs that share one must not be replayed at the
  * same time either). The workspace of paged_gqa_prefill_workspace_size(...,
- * PKV_KV_INT8) serves this call too. Batches above 8192 sequences, and batches
+ * PKV_KV_INT8) serves this call too, but not one that the f16 or FP8 calls
+ * use (see there: their counters lie elsewhere). Batches above 8192 sequences, and batches
  * of 2^31 or more (sequence, KV head, page) units, return
  * PKV_ERR_UNSUPPORTED.
  */

@@ -524,7 +524,8 @@ def paged_gqa_decode_workspace_size_int8() -> int:
 def paged_gqa_decode_attention_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, *,
                                     max_context_len, softmax_scale, workspace, stream=None) -> None:
     """paged_gqa_decode_attention over an 8-bit cache (load-balanced plan; a zero-filled workspace of
-    paged_gqa_decode_workspace_size_int8() bytes, reusable)."""
+    paged_gqa_decode_workspace_size_int8() bytes, reusable by the 8-bit calls; the f16 and FP8 calls keep
+    their counters elsewhere and need a workspace of their own)."""
     status = (_binding or _load_binding()).decode_attention_int8(
         out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, max_context_len, softmax_scale, workspace,
         stream)
@@ -536,7 +537,8 @@ def paged_gqa_prefill_attention_int8(out, q, k_cache, v_cache, kv_scales, block_
                                      max_query_len, max_context_len, softmax_scale, workspace, stream=None) -> None:
     """paged_gqa_prefill_attention over an 8-bit cache: query rows q [total, Hq, D] of each sequence
     (query_start [B+1] int32), the last n_b tokens of its context, attending causally; a zero-filled
-    workspace of paged_gqa_prefill_workspace_size(Hq, Hkv, D, "int8") bytes, reusable."""
+    workspace of paged_gqa_prefill_workspace_size(Hq, Hkv, D, "int8") bytes, reusable by the 8-bit calls
+    alone, as paged_gqa_decode_attention_int8's."""
     status = (_binding or _load_binding()).prefill_attention_int8(
         out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, max_query_len, max_context_len,
         softmax_scale, workspace, stream)
