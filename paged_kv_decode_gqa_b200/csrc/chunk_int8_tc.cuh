@@ -15,9 +15,9 @@
 // the keys rounded to f16 as well the output's error was 0.00032 of its norm,
 // where f16 outputs alone are off by 0.00019; it is 0.00025 so, at nearly the
 // same speed. With the values as exact codes too, their scales multiplied into the
-// weights, it was 0.00021, but 210 and 68 us instead of 174 and 59 for the two cases
-// below: the second factor per token doubles the reads of factors by every
-// softmax thread.)
+// weights, it was 0.00021, but 210 and 68 us instead of 170 and 59 for the two cases
+// below, timed as calls in a row: the second factor per token doubles the reads
+// of factors by every softmax thread.)
 //
 // Structure (one CTA per SM, persistent):
 //  * A query tile is T = floor(128 / G) query tokens x the G heads of one KV
@@ -54,13 +54,16 @@
 // Every wait is bounded; one that runs out flags PKV_DEVERR_WAIT_TIMEOUT and
 // every role stops, drains what it has in flight and leaves; TMEM is freed.
 //
-// Measured at 28 / 4 heads: 512 new tokens of 8 sequences on 2048-token contexts
-// 164 us, 0.39 of the measured dense rate; 5 new tokens of 64 sequences on
-// contexts of 32 to 2048 tokens 56 us. Bound: neither memory nor the tensor cores
-// but the chain S -> softmax -> P V of a stream, about 4500 cycles per KV tile of
-// which the products are 2300, on an SM whose shared memory is busy for 2560 of
-// them (operands 1536, conversion 768, TMA 256); and the instruction cache, which
-// the roles compete for. Tried and not kept, us for the two, against 160 / 54 of
+// Measured at 28 / 4 heads, in a graph: 512 new tokens of 8 sequences on 2048-token
+// contexts 165 us, 0.38 of the measured dense rate; 5 new tokens of 64 sequences on
+// contexts of 32 to 2048 tokens 57.7 us. Bound: neither memory nor the tensor cores.
+// A CTA takes about 5900 cycles per KV tile (wide: 280 thousand for 47.6 tiles, with
+// the launch, the scan and the merges), of which its tensor pipe is busy for 2050, as
+// long as the products take, and the threads' loads and stores keep shared memory busy
+// for 1690 beside the operands' 1536; narrow about 5800 and 1010. The rest is the
+// streams' chains S -> softmax -> P V, whose warps wait for tensor memory and for one
+// another more than for anything else, and the instruction cache, which the roles
+// compete for; how it divides among these has not been measured. Tried and not kept, us for the two, against 160 / 54 of
 // the form they started from (keys rounded to f16): logits in halves of 64 tokens,
 // double-buffered, one issuing warp 212 / 58 (products of N = 64 read Q twice); the
 // same with an issuing warp per stream 154 / 59; logits taken out of TMEM at once

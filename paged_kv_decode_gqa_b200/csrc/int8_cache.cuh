@@ -25,10 +25,11 @@
 // 4e-7, several times the rounding of the reduced angle to fp32.
 // Rounding: fp32 throughout, once to f16, to E4M3 (of x / scale, an IEEE
 // division, as paged_kv_cache_write) or to the 8-bit code.
-// Bound: HBM; every row is read and written once. Measured at 28 / 4 heads: f16,
-// 16384 tokens 52.9 us, 5.7 TB/s (0.87 of the measured copy rate); E4M3, 2049
-// tokens 5.9 us and f16, 128 tokens 2.8 us, where the launch and one round
-// trip to memory take most of it.
+// Bound: HBM; every row is read and written once. Measured in a graph: f16, 16384
+// tokens at 28 / 4 heads 52.6 us, 5.75 TB/s (0.88 of the measured copy rate), f16, 128
+// tokens of them 2.8 us, and E4M3, 2049 tokens at 12 / 2 heads 5.8 us, where the launch
+// and round trips to memory take most of it: one for the 128 tokens; two for the 2049,
+// whose 4098 shares of rows (two warps a token) the 2368 warps that fit take in two turns.
 #pragma once
 
 #include "cache_write.cuh"
@@ -368,7 +369,7 @@ struct RowWalk {
 
 // The write without rotation into an 8-bit cache: the K and V rows of all tokens in one run; a thread
 // keeps kRowBatch rows in flight and refills each as soon as it is done. Bound: HBM; 16411 tokens of 4 KV heads
-// written and read back (two launches, 102 MB) take 26.6 us, 0.59 of the measured copy rate.
+// written and read back (two launches, 102 MB) take 26.7 us, 0.58 of the measured copy rate.
 __global__ void __launch_bounds__(256, 4) cache_write_int8_kernel(const RopeWriteParams p) {
     const int i = threadIdx.x & 7;
     const int64_t groups = (int64_t)gridDim.x * 32;

@@ -778,7 +778,7 @@ bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 // ------------------------------------------- 8-bit cache, rotary cache write
 // Warps of a CTA and pages of a warp's ring: more warps hide one another's page update, deeper rings the
-// memory's latency. us for 128 sequences / 64 shorter ones / 8 with a long one, 28 / 4 heads:
+// memory's latency. us for 128 sequences / 64 shorter ones (12 / 2 heads) / 8 with a long one, 28 / 4 heads else:
 // 12 x 3 60.7 / 18.4 / 22.3, 12 x 4 60.4 / 18.9 / 22.2, 10 x 4 63.6 / 18.8 / 22.2, 14 x 3 61.3 / 19.3 / 22.8,
 // 16 x 3 59.9 / 19.2 / 22.7, 8 x 6 67.3 / 19.4 / 22.8.
 constexpr int kStreamWarps = 12, kStreamStages = 3;
@@ -1506,6 +1506,9 @@ pkv_status paged_gqa_prefill_attention_int8(void* out, const void* q, const void
     if (max_query_len > max_context_len) return PKV_ERR_INVALID_ARG;
     const int G = num_q_heads / num_kv_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // The streaming kernel holds 8 columns, and where it can serve a call it is the faster one: us of it / of the
+    // tensor-core kernel at 28 / 4 heads, one query (7 columns): 64 sequences of 32 to 2048 tokens 23.3 / 54.4, 128
+    // of 512 to 4096 58.8 / 161, one of 2000 11.7 / 17.4; at 8 / 8 heads 1 query 34.0 / 91.5, 8 queries 36.2 / 92.7.
     if (max_query_len * (int64_t)G <= 8 && stream_fits(batch, num_kv_heads, max_context_len)) {
         pkv::StreamInt8Params prm{};
         prm.out = static_cast<__half*>(out);

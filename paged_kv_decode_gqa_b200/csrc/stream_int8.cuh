@@ -35,11 +35,14 @@
 // 0. A scale outside [0, 2^60] is flagged and counts as 0, a row of zeros
 // (V: 2^-60 in its place, which rounds to zeros in any f16 output).
 //
-// Bound: HBM. Bytes of a unit: 2 x 16 x (128 + 4). Measured at 28 / 4 heads: 128
-// sequences of 512 to 4096 tokens 59.0 us, 0.81 of the measured copy rate; 64
-// sequences of 32 to 2048 tokens (35.5 MB) 18.2 us and 8 with one of 32768
-// (39 MB) 21.8 us, where the launch, the scan of the lengths, the first loads
-// and the merge tree are about 10 us that no byte hides.
+// Bound: HBM. Bytes of a unit: 2 x 16 x (128 + 4). Measured in a graph (called in a
+// row in brackets): at 28 / 4 heads 128 sequences of 512 to 4096 tokens 58.9 us (63.1),
+// 0.81 (0.76) of the measured copy rate; 64 sequences of 32 to 2048 tokens at 12 / 2
+// heads (35.5 MB) 18.1 us (18.6), and 8 sequences, one of 32768 tokens, at 28 / 4 heads
+// (39 MB) 21.7 us (22.2), where the launch, the scan of the lengths, the first loads
+// and the merges, which no byte hides, take about two thirds: a batch of two short
+// sequences, which has little else, takes 6.8 us, and the merges of many pieces by
+// one warp each the rest.
 #pragma once
 
 #include <type_traits>
