@@ -30,6 +30,8 @@ def bound_of(c, scale=SCALE):
     for b in range(c.B):
         r0, r1, L = int(c.qs[b]), int(c.qs[b + 1]), int(c.lens[b])
         n = r1 - r0
+        if L == 0 or n == 0:
+            continue
         blk, row = c.rows_of(b)
         hidden = np.arange(L)[None, :] > (L - n + np.arange(n))[:, None]
         for h in range(c.Hq):
